@@ -24,6 +24,7 @@ lib = ctypes.CDLL(LIB)
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE, DSA_ERR_CUDA = range(5)
 DSA_DEVERR_BLOCK_OOB, DSA_DEVERR_INDEX_OOB, DSA_DEVERR_TIMEOUT, DSA_DEVERR_SEQ_LEN = 1, 2, 4, 8
+DSA_DEVERR_NO_BLOCKS = 16
 DSA_KV_SPLITS_BATCH_INVARIANT = -1
 
 _p = ctypes.c_void_p
@@ -61,6 +62,13 @@ _SIGS = {
                                 _f32, _p, _p, _p, _p], _i32),
     "dsa_mla_kv_fp8_quant_and_cache": ([_p, _i64, _i32, _i32, _i32, _p, _i64, _i32, _p, _i32, _p, _p, _i32, _i32, _p,
                                         _p], _i32),
+    "dsa_build_batch": ([_p, _p, _i32, _i32, _p, _i32, _p, _p, _p, _i32, _i32, _p, _p, _p, _p, _p, _p, _p], _i32),
+    "dsa_mla_kv_cache": ([_p, _i64, _i32, _i32, _p, _p, _i64, _i32, _i32, _p, _p], _i32),
+    "dense_mla_workspace_size": ([_i32, _i32, _i32, _i32], _sz),
+    "dense_mla_attention": ([_p, _p, _i64, _i32, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _p,
+                             _p, _p, _sz, _p, _p], _i32),
+    "dense_mla_attention_fp8": ([_p, _p, _i64, _i32, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32,
+                                 _p, _p, _p, _sz, _p, _p], _i32),
 }
 
 MLA_FP8_ROW_BYTES = 656  # fp8 latent cache row at Dk = 576, Dv = 512
@@ -385,3 +393,140 @@ def dsa_mla_kv_fp8_quant_and_cache(kv, kv_cache, block_table, seq_lens, query_st
                                             seq_lens.shape[0], block_size, _ptr(dev_status), _stream(stream))
     _check(st, "dsa_mla_kv_fp8_quant_and_cache")
     return kv_cache
+
+
+def _same_device(**tensors):
+    """Every tensor given lies on the current CUDA device, whose stream and kernels the call uses."""
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+
+
+def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, free_blocks=None, free_head=None,
+                    free_head_out=None, seq_lens=None, query_start_loc=None, token_req=None, positions=None,
+                    slot_map=None, dev_status=None, stream=None):
+    """The batch's metadata from its lengths, on the device: returns
+    (seq_lens [B], query_start_loc [B+1], token_req, positions, slot_map
+    [max_tokens]) and grows block_table [B, bt_stride] in place by blocks of
+    the queue free_blocks, from *free_head on; free_head_out (default: in
+    place) receives the advanced head."""
+    _need(ctx_lens, torch.int32, "ctx_lens", 1)
+    _need(new_lens, torch.int32, "new_lens", 1)
+    _need(block_table, torch.int32, "block_table", 2)
+    B, dev = ctx_lens.shape[0], ctx_lens.device
+    if new_lens.shape[0] != B or block_table.shape[0] < B:
+        raise ValueError("new_lens and block_table must have a row per request of ctx_lens")
+    if free_blocks is not None:
+        _need(free_blocks, torch.int32, "free_blocks", 1)
+        free_head_out = free_head if free_head_out is None else free_head_out
+        _need(free_head, torch.int32, "free_head", 1)
+        _need(free_head_out, torch.int32, "free_head_out", 1)
+        if free_head.numel() < 1 or free_head_out.numel() < 1:
+            raise ValueError("free_head and free_head_out must have an element")
+    outs = {}
+    for name, t, n, dt in (("seq_lens", seq_lens, B, torch.int32),
+                           ("query_start_loc", query_start_loc, B + 1, torch.int32),
+                           ("token_req", token_req, max_tokens, torch.int32),
+                           ("positions", positions, max_tokens, torch.int32),
+                           ("slot_map", slot_map, max_tokens, torch.int64)):
+        if t is None:
+            t = torch.empty(max(n, 0), dtype=dt, device=dev)
+        _need(t, dt, name, 1)
+        if t.shape[0] < n:
+            raise ValueError(f"{name} needs {n} elements, has {t.shape[0]}")
+        outs[name] = t
+    if dev_status is not None:
+        _need(dev_status, torch.int32, "dev_status")
+    _same_device(ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table, free_blocks=free_blocks,
+                 free_head=free_head, free_head_out=free_head_out, dev_status=dev_status, **outs)
+    # an empty queue has no address of its own, and NULL would mean "take no blocks"
+    queue = free_blocks if free_blocks is None or free_blocks.numel() else free_head
+    st = lib.dsa_build_batch(_ptr(ctx_lens), _ptr(new_lens), B, block_size, _ptr(queue),
+                             0 if free_blocks is None else free_blocks.shape[0], _ptr(free_head), _ptr(free_head_out),
+                             _ptr(block_table), block_table.shape[1], max_tokens, _ptr(outs["seq_lens"]),
+                             _ptr(outs["query_start_loc"]), _ptr(outs["token_req"]), _ptr(outs["positions"]),
+                             _ptr(outs["slot_map"]), _ptr(dev_status), _stream(stream))
+    _check(st, "dsa_build_batch")
+    return tuple(outs.values())
+
+
+def dsa_mla_kv_cache(kv, slot_map, kv_cache, dev_status=None, stream=None):
+    """Stores the latent rows kv [T, Dk] (bf16; rows may be strided) at their
+    slots (int64 [T], -1 = skip) of the bf16 latent cache kv_cache
+    [num_blocks, block_size, Dk] in place."""
+    if not isinstance(kv, torch.Tensor) or kv.dtype != torch.bfloat16 or kv.dim() != 2 or not kv.is_cuda:
+        raise TypeError("kv must be a two-dimensional bfloat16 CUDA tensor")
+    T, Dk = kv.shape
+    if Dk > 1 and kv.stride(1) != 1:
+        raise ValueError("the values of a row of kv must be contiguous")
+    _need(slot_map, torch.int64, "slot_map", 1)
+    _need(kv_cache, torch.bfloat16, "kv_cache", 3)
+    if slot_map.shape[0] < T or kv_cache.shape[2] != Dk:
+        raise ValueError("slot_map needs an entry per row of kv, and kv_cache rows as wide as kv's")
+    if dev_status is not None:
+        _need(dev_status, torch.int32, "dev_status")
+    _same_device(kv=kv, slot_map=slot_map, kv_cache=kv_cache, dev_status=dev_status)
+    nb, bs, _ = kv_cache.shape
+    st = lib.dsa_mla_kv_cache(_ptr(kv), kv.stride(0) if T > 1 else Dk, T, Dk, _ptr(slot_map), _ptr(kv_cache), bs * Dk,
+                              nb, bs, _ptr(dev_status), _stream(stream))
+    _check(st, "dsa_mla_kv_cache")
+    return kv_cache
+
+
+def dense_mla_workspace_size(T: int, H: int, Dv: int, num_kv_splits: int) -> int:
+    return int(lib.dense_mla_workspace_size(T, H, Dv, num_kv_splits))
+
+
+def _dense_mla(name, q, kv_cache, cache_dtype, block_table, seq_lens, query_start_loc, softmax_scale, dv, out, lse,
+               num_kv_splits, workspace, dev_status, stream):
+    _need(q, torch.bfloat16, "q", 3)
+    _need(kv_cache, cache_dtype, "kv_cache", 3)
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _need(query_start_loc, torch.int32, "query_start_loc", 1)
+    _need(out, torch.bfloat16, "out", 3)
+    T, H, Dk = q.shape
+    B = seq_lens.shape[0]
+    num_blocks, block_size, row = kv_cache.shape
+    if tuple(out.shape) != (T, H, dv):
+        raise ValueError(f"out must be {(T, H, dv)}, got {tuple(out.shape)}")
+    if row != (Dk if cache_dtype == torch.bfloat16 else MLA_FP8_ROW_BYTES):
+        raise ValueError(f"kv_cache rows of {row} elements do not fit q's {Dk} dims")
+    if block_table.shape[0] < B or query_start_loc.shape[0] != B + 1:
+        raise ValueError("block_table needs a row per request, query_start_loc one entry more than seq_lens")
+    if lse is not None:
+        _need(lse, torch.float32, "lse", 2)
+        if tuple(lse.shape) != (T, H):
+            raise ValueError(f"lse must be {(T, H)}, got {tuple(lse.shape)}")
+    if dev_status is not None:
+        _need(dev_status, torch.int32, "dev_status")
+    need = dense_mla_workspace_size(T, H, dv, num_kv_splits)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _same_device(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, query_start_loc=query_start_loc,
+                 out=out, lse=lse, workspace=workspace, dev_status=dev_status)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = getattr(lib, name)(_ptr(q), _ptr(kv_cache), block_size * row, num_blocks, _ptr(block_table),
+                            block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc), B, T, H, Dk, dv, block_size,
+                            softmax_scale, num_kv_splits, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+                            _ptr(dev_status), _stream(stream))
+    _check(st, name)
+    return out
+
+
+def dense_mla_attention(q, kv_cache, block_table, seq_lens, query_start_loc, softmax_scale, dv, out, lse=None,
+                        num_kv_splits=0, workspace=None, dev_status=None, stream=None):
+    """Dense causal MLA of new tokens q [T,H,Dk] over the paged bf16 latent
+    cache [blocks, block_size, Dk]: out [T,H,Dv] (bf16), lse [T,H].
+    num_kv_splits: 0 spreads the keys over the GPU, -1 or 1 never cuts a
+    token's keys (results independent of the batch)."""
+    return _dense_mla("dense_mla_attention", q, kv_cache, torch.bfloat16, block_table, seq_lens, query_start_loc,
+                      softmax_scale, dv, out, lse, num_kv_splits, workspace, dev_status, stream)
+
+
+def dense_mla_attention_fp8(q, kv_cache, block_table, seq_lens, query_start_loc, softmax_scale, dv, out, lse=None,
+                            num_kv_splits=0, workspace=None, dev_status=None, stream=None):
+    """dense_mla_attention over the fp8 latent cache [blocks, block_size, 656] (uint8)."""
+    return _dense_mla("dense_mla_attention_fp8", q, kv_cache, torch.uint8, block_table, seq_lens, query_start_loc,
+                      softmax_scale, dv, out, lse, num_kv_splits, workspace, dev_status, stream)

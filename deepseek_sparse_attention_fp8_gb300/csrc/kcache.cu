@@ -174,10 +174,59 @@ __global__ void __launch_bounds__(kThreads) mla_kv_fp8_cache_kernel(const uint16
   if (lane < 8) *reinterpret_cast<uint4*>(row + kF8Dv + 16 + 16 * lane) = rope;
 }
 
+// Producer side of the bf16 latent cache: token t's row goes to the slot the
+// caller gives. A copy of Dk bf16 per token, 16 bytes per thread; its floor is
+// the rows read and written once.
+__global__ void __launch_bounds__(kThreads) mla_kv_cache_kernel(const uint4* kv, int64_t kv_stride, int64_t n_chunks,
+                                                                int row_chunks, const int64_t* slot_map, uint4* cache,
+                                                                int64_t block_stride, int64_t n_slots, int block_size,
+                                                                int32_t* dev_status) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= n_chunks) return;
+  const int64_t t = i / row_chunks;
+  const int c = static_cast<int>(i - t * row_chunks);
+  const int64_t slot = __ldg(slot_map + t);
+  if (slot < 0 || slot >= n_slots) {
+    if (slot != -1 && c == 0) report(dev_status, DSA_DEVERR_BLOCK_OOB);
+    return;
+  }
+  const int64_t blk = slot / block_size;
+  cache[blk * block_stride + (slot - blk * block_size) * row_chunks + c] = __ldg(kv + t * kv_stride + c);
+}
+
 }  // namespace
 }  // namespace dsa
 
 using namespace dsa;
+
+extern "C" dsa_status_t dsa_mla_kv_cache(const void* kv, int64_t kv_stride_t, int32_t T, int32_t Dk,
+                                         const int64_t* slot_map, void* kv_cache, int64_t kv_block_stride,
+                                         int32_t num_blocks, int32_t block_size, int32_t* dev_status,
+                                         dsa_stream_t stream) {
+  if (T < 0 || Dk <= 0 || block_size <= 0 || num_blocks < 0)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_mla_kv_cache: negative or zero size argument");
+  if (Dk % 8) return fail(DSA_ERR_UNSUPPORTED, "dsa_mla_kv_cache: Dk=%d not a multiple of 8", Dk);
+  if (block_size % 64)
+    return fail(DSA_ERR_UNSUPPORTED, "dsa_mla_kv_cache: block_size %d not a multiple of 64", block_size);
+  if (T == 0) return DSA_OK;
+  if (!kv || !slot_map || !kv_cache) return fail(DSA_ERR_INVALID_ARG, "dsa_mla_kv_cache: null pointer");
+  if (kv_block_stride < static_cast<int64_t>(block_size) * Dk || kv_block_stride % 8)
+    return fail(DSA_ERR_INVALID_ARG,
+                "dsa_mla_kv_cache: kv_block_stride %lld must be >= block_size rows of %d and a multiple of 8",
+                static_cast<long long>(kv_block_stride), Dk);
+  if (!aligned16(kv) || !aligned16(kv_cache) || kv_stride_t < Dk || kv_stride_t % 8)
+    return fail(DSA_ERR_INVALID_ARG,
+                "dsa_mla_kv_cache: kv/kv_cache must be 16-byte aligned, token stride >= Dk and a multiple of 8");
+  dsa_status_t st = check_device();
+  if (st != DSA_OK) return st;
+  const int row_chunks = Dk / 8;
+  const int64_t n = static_cast<int64_t>(T) * row_chunks, grid = (n + kThreads - 1) / kThreads;
+  if (grid > 0x7FFFFFFF) return fail(DSA_ERR_UNSUPPORTED, "dsa_mla_kv_cache: grid too large");
+  mla_kv_cache_kernel<<<static_cast<unsigned>(grid), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      static_cast<const uint4*>(kv), kv_stride_t / 8, n, row_chunks, slot_map, static_cast<uint4*>(kv_cache),
+      kv_block_stride / 8, static_cast<int64_t>(num_blocks) * block_size, block_size, dev_status);
+  return check_launch("mla_kv_cache_kernel");
+}
 
 extern "C" dsa_status_t dsa_mla_kv_fp8_quant_and_cache(const void* kv, int64_t kv_stride_t, int32_t T, int32_t Dk,
                                                        int32_t Dv, uint8_t* kv_cache, int64_t kv_block_stride_bytes,

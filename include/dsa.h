@@ -94,6 +94,7 @@ typedef enum {
 #define DSA_DEVERR_INDEX_OOB 2u /* a top-k index outside [-1, valid(t)) was given */
 #define DSA_DEVERR_TIMEOUT 4u   /* a bounded wait inside a kernel ran out */
 #define DSA_DEVERR_SEQ_LEN 8u   /* seq_lens[b] < q_len_b, or larger than the block table can hold */
+#define DSA_DEVERR_NO_BLOCKS 16u /* dsa_build_batch: the queue of free blocks ran out */
 
 /* num_kv_splits value of sparse_mla_decode that makes the split count depend
  * on index_topk alone, so a token's out and lse do not depend on the batch. */
@@ -315,6 +316,108 @@ dsa_status_t dsa_mla_kv_fp8_quant_and_cache(const void* kv, int64_t kv_stride_t,
                                             const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
                                             const int32_t* query_start_loc, int32_t B, int32_t block_size,
                                             int32_t* dev_status, dsa_stream_t stream);
+
+/*
+ * Batch metadata built on the device: from every request's cached and new
+ * token counts, the arrays that the other calls take (seq_lens,
+ * query_start_loc, the block table grown by the blocks the new tokens need)
+ * and, per query token, its request, position and cache slot. Nothing of it
+ * passes through the host, so a serving loop can capture it in a CUDA graph.
+ *   ctx_lens   int32 [B]  keys already cached (0 for a new prompt)
+ *   new_lens   int32 [B]  query tokens of this step (0 for an idle request)
+ *   block_table int32 [B, bt_stride], in and out: row b holds the
+ *              ceil(ctx/block_size) blocks of the cached keys; the blocks up
+ *              to ceil((ctx+new)/block_size) are taken from the free queue,
+ *              request by request in order, and stored. No other entry is
+ *              touched.
+ *   free_blocks int32 [num_free]  queue of free block ids, taken from
+ *              free_blocks[*free_head] on; *free_head_out receives the
+ *              advanced head (it may be the same address as free_head, so
+ *              that a replayed graph moves it along). free_blocks = NULL: no
+ *              block is taken, the table already holds every block needed,
+ *              and free_head and free_head_out are not used.
+ *   seq_lens   int32 [B]      ctx + new
+ *   query_start_loc int32 [B+1]  exclusive prefix sum of new
+ *   token_req, positions int32 [max_tokens], slot_map int64 [max_tokens]:
+ *              of query token t its request b, its position ctx[b] + t -
+ *              query_start_loc[b] and its cache slot block * block_size +
+ *              position % block_size. Rows from the batch's token count up to
+ *              max_tokens (a padded buffer) get -1, 0 and -1.
+ * What only the device sees: a negative length, or one whose ctx + new passes
+ * 2^31 - 1, counts as 0 new tokens (and a negative ctx as 0); new tokens past
+ * max_tokens are dropped from the batch, the last requests' first; both set
+ * DSA_DEVERR_SEQ_LEN. Tokens past the table's bt_stride blocks
+ * (DSA_DEVERR_SEQ_LEN), tokens for which no free block is left or whose head
+ * lies outside [0, num_free] (DSA_DEVERR_NO_BLOCKS; the entry becomes -1) and
+ * tokens whose table entry or free id is negative (DSA_DEVERR_BLOCK_OOB) get
+ * slot -1.
+ */
+dsa_status_t dsa_build_batch(const int32_t* ctx_lens, const int32_t* new_lens, int32_t B, int32_t block_size,
+                             const int32_t* free_blocks, int32_t num_free, const int32_t* free_head,
+                             int32_t* free_head_out, int32_t* block_table, int32_t bt_stride, int32_t max_tokens,
+                             int32_t* seq_lens, int32_t* query_start_loc, int32_t* token_req, int32_t* positions,
+                             int64_t* slot_map, int32_t* dev_status, dsa_stream_t stream);
+
+/*
+ * Producer side of the bf16 latent cache: stores the latent rows of T tokens
+ * at their slots (dsa_build_batch's slot_map).
+ *   kv       bf16 [T, Dk], token stride kv_stride_t elements (>= Dk, a
+ *            multiple of 8; 16-byte aligned)
+ *   slot_map int64 [T]: row slot % block_size of block slot / block_size; -1
+ *            skips the token, any other value outside [0, num_blocks *
+ *            block_size) skips it and sets DSA_DEVERR_BLOCK_OOB. Tokens must
+ *            not share a slot.
+ *   kv_cache the bf16 latent cache, written in place; nothing else of it is
+ *            touched.
+ * Supported: Dk a multiple of 8, block_size a multiple of 64.
+ */
+dsa_status_t dsa_mla_kv_cache(const void* kv, int64_t kv_stride_t, int32_t T, int32_t Dk, const int64_t* slot_map,
+                              void* kv_cache, int64_t kv_block_stride, int32_t num_blocks, int32_t block_size,
+                              int32_t* dev_status, dsa_stream_t stream);
+
+/*
+ * Dense MLA attention of new tokens over the paged latent cache: what a3
+ * computes, over all keys a token may see instead of selected ones. For
+ * requests not longer than index_topk, dense layers, and chunks of a prompt
+ * (one token to many thousands per request, mixed in one batch).
+ *   q         bf16 [T, H, Dk] (contiguous)
+ *   kv_cache  bf16 paged latent cache, the new tokens' rows already stored
+ *   out       bf16 [T, H, Dv]: softmax(scale * q . kv[s]) @ kv[s, :Dv] over
+ *             the keys s < valid(t)
+ *   lse       fp32 [T, H] natural-log sum-exp of the scaled scores, or NULL.
+ * T is the tokens' buffer size: rows of out and lse from query_start_loc[B]
+ * on (a padded batch) are left as they were. Cached values at positions below
+ * seq_lens[b] must be finite, whatever lies behind them in the last block is
+ * not used. A token without a key (seq_lens[b] < q_len_b,
+ * DSA_DEVERR_SEQ_LEN) gets out = 0 and lse = -inf; keys past the block table
+ * (DSA_DEVERR_SEQ_LEN) and keys of blocks outside [0, num_blocks)
+ * (DSA_DEVERR_BLOCK_OOB) count as masked.
+ * num_kv_splits: 0 spreads the keys evenly over the GPU, cutting a token's
+ * keys where that falls (the cuts, and so the last bits of out and lse, depend
+ * on the batch); DSA_KV_SPLITS_BATCH_INVARIANT (-1) or 1 never cuts, so a
+ * token's results do not depend on the other requests of the batch.
+ * `workspace` takes dense_mla_workspace_size() bytes (16-byte aligned); with
+ * -1 or 1 none. Its size does not grow with the context. Calls that may
+ * overlap on the GPU need a workspace each.
+ * Supported: (Dk, Dv) = (576, 512), H <= 128, block_size a multiple of 64.
+ */
+size_t dense_mla_workspace_size(int32_t T, int32_t H, int32_t Dv, int32_t num_kv_splits);
+dsa_status_t dense_mla_attention(const void* q, const void* kv_cache, int64_t kv_block_stride, int32_t num_blocks,
+                                 const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                 const int32_t* query_start_loc, int32_t B, int32_t T, int32_t H, int32_t Dk,
+                                 int32_t Dv, int32_t block_size, float softmax_scale, int32_t num_kv_splits, void* out,
+                                 float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                 dsa_stream_t stream);
+
+/*
+ * The same over the fp8 latent cache (kv_block_stride_bytes in bytes).
+ */
+dsa_status_t dense_mla_attention_fp8(const void* q, const uint8_t* kv_cache, int64_t kv_block_stride_bytes,
+                                     int32_t num_blocks, const int32_t* block_table, int32_t bt_stride,
+                                     const int32_t* seq_lens, const int32_t* query_start_loc, int32_t B, int32_t T,
+                                     int32_t H, int32_t Dk, int32_t Dv, int32_t block_size, float softmax_scale,
+                                     int32_t num_kv_splits, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                     int32_t* dev_status, dsa_stream_t stream);
 
 /*
  * Split-KV sparse MLA decode that allocates nothing. It serves callers that
