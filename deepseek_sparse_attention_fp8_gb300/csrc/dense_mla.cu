@@ -4,12 +4,30 @@
 //   s_i = scale * q[t,h,:] . kv[i,:]   for the keys i <= pos
 //   out = sum_i softmax(s)_i * kv[i, :512]     lse = log sum_i exp(s_i)
 //
-// The simple form: one warp per (token, head), the 8 warps of a CTA taking 8
-// heads of a token; a lane holds dims {2 lane + 64 i, 2 lane + 64 i + 1} of q
-// and of the output, and the softmax runs over the keys one at a time.
+// Rows: the (token, head) rows of a request, 128 / H whole tokens at a time,
+// form row tiles of at most 128 rows; all of them see the same latent rows. A
+// row tile is worked on by a CTA pair, in steps of 128 keys:
+//   S = Q K^T   one cta_group::2 MMA, M = 128 (64 rows per CTA), N = 128:
+//               each CTA brings the 64 q rows it owns and 64 of the keys;
+//   softmax     thread = row and 32 keys; lazy rescaling of O (only when the
+//               row maximum grows by more than 2^8);
+//   O += P V    M = 128, N = 2 x 256: CTA r brings its rows of P and value
+//               dims [256 r, 256 r + 256) of all 128 keys.
+// CTA r needs all dims of its own 64 keys for S, and its own 256 dims of the
+// other 64 keys for O. The MMA takes the same offsets in both CTAs, so the
+// blocks of the other keys replace, after S, exactly those blocks of the own
+// keys that O does not need: a step holds 64 KB per CTA, and two steps are in
+// flight. A step moves 104 KB into each SM; at the ~32 bytes per clock that
+// an SM takes in (measured: 62 GB/s, whether from L2 or memory, multicast or
+// not) that is 3330 clocks, against 2180 of MMA: the copies bound it.
+//
+// Work: the steps of all row tiles form one sequence, cut into equal runs, one
+// per CTA pair (one persistent wave). A row tile cut by a run's end leaves
+// fp32 partials, at most two per pair, joined by dense_mla_merge_kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -18,11 +36,763 @@
 namespace dsa {
 namespace {
 
+using namespace ptx;
+
 constexpr int kDk = 576, kDv = 512, kF8Row = 656;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+constexpr int kThreads = 352;  // warps 0-7 softmax, 8 keys, 9 q / rope / other keys, 10 MMA
+constexpr int kKeyWarp = 8, kAuxWarp = 9, kMmaWarp = 10;
+constexpr int kTile = 128;
+constexpr int kSlot = 16384;  // 64 keys x 128 dims
+constexpr float kRescaleThreshold = 8.f;  // log2 units
+constexpr long long kWaitLimitCycles = 2000000000ll;
+constexpr int kMinRun = 4;  // steps a run has at least when row tiles may be cut
+constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;  // O 256 columns, S 2 x 64
+
+// Shared memory: q as 9 blocks of 64 rows x 64 dims, two steps of 4 key slots,
+// the rope dims of a step's own keys, P as 2 blocks of 64 rows x 64 keys (all
+// 128-byte swizzled), row maxima [2][4][64], barriers.
+constexpr int kSmQ = 0, kSmKv = kSmQ + 9 * 8192, kSmRope = kSmKv + 8 * kSlot, kSmP = kSmRope + 8192,
+              kSmRed = kSmP + 2 * 8192, kSmBar = kSmRed + 2 * 4 * 64 * 4, kSmTotal = kSmBar + 512;
+static_assert(kSmTotal <= 232448, "more than 227 KB of shared memory");
+
+struct Bars {
+  uint64_t full[2][4];   // a slot's own keys, of both CTAs (the even CTA's barrier)
+  uint64_t other[2];     // a step's other keys, of both CTAs (the even CTA's)
+  uint64_t rope, q;      // (the even CTA's)
+  uint64_t p_full;       // P written by the 16 softmax warps of the pair (the even CTA's)
+  uint64_t s_full[2];    // S of a step complete (in both CTAs)
+  uint64_t pv_done[2];   // O += P V of a step complete (in both CTAs)
+  uint64_t rows[2];      // the four softmax warps that share 32 rows
+  uint32_t tmem;
+  volatile int abort;
+  // the run: first request, row tile and step of it, and the units [pos, end)
+  int32_t b, tile, k0, pad;
+  int64_t pos, end, per, total;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block too large");
+
 struct DenseParams {
+  int32_t num_blocks, rows_per_block, total_rows;
+  const int32_t* block_table;
+  int32_t bt_stride;
+  const int32_t *seq_lens, *qsl;
+  int32_t B, T, H, tpt;      // tpt: tokens per row tile
+  int32_t block_size, bs64;  // bs64 = block_size / 64
+  float scale_log2;
+  int32_t cut;    // row tiles may be cut
+  int32_t out32;  // out is 32-byte aligned
+  uint16_t* out;
+  float* lse;
+  float4* o_part;   // [2 per pair][2 CTAs][64 column groups][128 lanes]
+  float2* ml_part;  // [2 per pair][128 rows]: max (log2 units), sum
+  int4* desc;       // per pair: the cut row tile that starts in its run
+  int32_t* dev_status;
+};
+
+// A request's rows as work: row tile i has steps(i) = max(1, ceil(keys its
+// last token sees / 128)).
+struct Request {
+  int32_t q0, q_len, n_tiles, kv_len;  // kv_len: its cached keys that the table can hold
+  int64_t c;     // position of its first new token
+  bool uneven;   // lengths that contradict each other: every tile is charged kv_len
+};
+
+__device__ __forceinline__ Request load_request(const DenseParams& p, int b) {
+  Request r;
+  const int q0 = min(max(__ldg(p.qsl + b), 0), p.T), q1 = min(max(__ldg(p.qsl + b + 1), 0), p.T);
+  const int64_t sl = __ldg(p.seq_lens + b), cap = static_cast<int64_t>(p.bt_stride) * p.block_size;
+  r.q0 = q0;
+  r.q_len = max(q1 - q0, 0);
+  r.n_tiles = (r.q_len + p.tpt - 1) / p.tpt;
+  r.kv_len = static_cast<int32_t>(max(int64_t(0), min(min(sl, cap), int64_t(0x7FFFFF00))));
+  r.c = sl - r.q_len;
+  r.uneven = r.c < 0 || r.kv_len != sl;
+  return r;
+}
+// keys visible to the token i (from 0) of the request
+__device__ __forceinline__ int visible(const Request& r, int i) {
+  return static_cast<int>(max(int64_t(0), min(r.c + i + 1, int64_t(r.kv_len))));
+}
+__device__ __forceinline__ int steps_of(const DenseParams& p, const Request& r, int tile) {
+  const int keys = r.uneven ? r.kv_len : visible(r, min(r.q_len, (tile + 1) * p.tpt) - 1);
+  return max(1, static_cast<int>((static_cast<int64_t>(keys) + kTile - 1) / kTile));
+}
+// sum over i < n of floor((a i + b) / 128)
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
+  if ((a & (a - 1)) == 0) {  // a divides 128: floor((i + b / a) / (128 / a)), a whole run of each quotient
+    const int sh = 7 - (31 - __clz(static_cast<int>(a)));
+    const auto upto = [&](int64_t x) {  // sum over j < x of floor(j / 2^sh)
+      const int64_t k = x >> sh;
+      return ((k * (k - 1) / 2) << sh) + k * (x & ((int64_t(1) << sh) - 1));
+    };
+    const int64_t b0 = b / a;
+    return upto(n + b0) - upto(b0);
+  }
+  // the lattice points under the line, by the Euclidean algorithm
+  int64_t sum = 0, m = 128;
+  while (true) {
+    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const int64_t top = a * n + b;
+    if (top < m) return sum;
+    n = top / m;
+    b = top % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+}
+// steps of the request's row tiles before tile n
+__device__ __forceinline__ int64_t steps_before(const DenseParams& p, const Request& r, int n) {
+  if (r.uneven) return static_cast<int64_t>(n) * steps_of(p, r, 0);
+  if (n == 0) return 0;
+  if (n < r.n_tiles) return floor_sum(n, p.tpt, r.c + p.tpt + kTile - 1);
+  return floor_sum(n - 1, p.tpt, r.c + p.tpt + kTile - 1) + steps_of(p, r, n - 1);
+}
+
+// A run of steps, segment by segment (a segment: the steps of one row tile).
+struct Cursor {
+  Request req;
+  int32_t b, tile, nk, k0, k1;
+  int64_t pos, end;
+  __device__ __forceinline__ void cut(const DenseParams& p) {
+    nk = steps_of(p, req, tile);
+    k1 = nk;
+    if (p.cut && end - pos < k1 - k0) k1 = k0 + static_cast<int32_t>(end - pos);
+  }
+  __device__ __forceinline__ bool start(const DenseParams& p, const Bars* s) {
+    b = s->b;
+    tile = s->tile;
+    k0 = s->k0;
+    pos = s->pos;
+    end = s->end;
+    if (pos >= end) return false;
+    req = load_request(p, b);
+    cut(p);
+    return true;
+  }
+  __device__ __forceinline__ bool next(const DenseParams& p) {
+    pos += k1 - k0;
+    if (pos >= end) return false;
+    k0 = 0;
+    if (++tile >= req.n_tiles) {
+      tile = 0;
+      do {
+        if (++b >= p.B) return false;
+        req = load_request(p, b);
+      } while (req.n_tiles == 0);
+    }
+    cut(p);
+    return true;
+  }
+};
+
+// The cache rows of 64 keys from key0 on: their first row (total_rows, which
+// reads as zeros, where there is none) and how many of them exist.
+struct Rows {
+  int32_t row, n;
+};
+__device__ __forceinline__ Rows rows_of(const DenseParams& p, int b, int kv_len, int key64, bool rep) {
+  Rows x{p.total_rows, 0};
+  const int left = kv_len - key64 * 64;
+  if (left <= 0) return x;
+  const int j = key64 / p.bs64;
+  const int blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.bt_stride + j);
+  if (blk < 0 || blk >= p.num_blocks) {
+    if (rep) report(p.dev_status, DSA_DEVERR_BLOCK_OOB);
+    return x;
+  }
+  x.row = blk * p.rows_per_block + (key64 - j * p.bs64) * 64;
+  x.n = min(left, 64);
+  return x;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// mbar_wait with one answer for the warp
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+}
+
+// Loads 64 keys x 64 * blocks dims (dim block d0 on) by the whole warp. The
+// rows behind a request's last key are not its own and may hold anything,
+// NaN included, so they are gathered from past the cache's end, as zeros.
+__device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* box, const CUtensorMap* row_map,
+                                          uint32_t bar, Rows x, int32_t total_rows, int d0, int blocks, int lane) {
+  if (x.n == 0 || x.n == 64) {
+    if (lane == 0) tma_load_3d_pair(dst, box, bar, 0, x.row, d0);
+  } else {
+    const int g = lane & 15, d = lane >> 4;
+    if (d < blocks) {
+      int r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = 4 * g + i < x.n ? x.row + 4 * g + i : total_rows;
+      tma_gather4_pair(dst + d * 8192 + g * 512, row_map, bar, (d0 + d) * 64, r[0], r[1], r[2], r[3]);
+    }
+  }
+  __syncwarp();
+}
+
+// The run of this pair: every CTA sums the requests' steps itself. `scratch`
+// is shared memory that nothing else uses yet.
+__device__ __forceinline__ void plan_run(const DenseParams& p, Bars* s, uint8_t* scratch, int pair, int n_pairs) {
+  int64_t* sums = reinterpret_cast<int64_t*>(scratch);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kThreads / 32;
+  const bool once = p.B <= kThreads;
+  int64_t w = 0, incl = 0;
+  Request r = {};
+  const auto scan = [&](int b) {  // steps of request b, and their inclusive sum over the block's requests
+    w = 0;
+    if (b < p.B) {
+      r = load_request(p, b);
+      if (r.uneven && r.q_len > 0 && pair == 0) {
+        const int64_t sl = r.c + r.q_len;
+        if (sl > r.kv_len || r.c < 0) report(p.dev_status, DSA_DEVERR_SEQ_LEN);
+      }
+      w = steps_before(p, r, r.n_tiles);
+    }
+    incl = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+      if (lane >= off) incl += u;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int64_t all = 0;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) incl += sums[i];
+      all += sums[i];
+    }
+    return all;
+  };
+  int64_t total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) total += scan(b0 + tid);
+  int64_t per = (total + n_pairs - 1) / n_pairs;
+  if (p.cut) per = max(per, int64_t(kMinRun));
+  const int64_t u0 = per * pair, u1 = min(u0 + per, total);
+  if (tid == 0) {
+    s->per = per;
+    s->total = total;
+    s->pos = s->end = 0;
+  }
+  __syncthreads();
+  if (u0 < u1) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int64_t all = once ? total : scan(b0 + tid);
+      const int64_t from = base + incl - w;
+      if (w > 0 && from <= u0 && u0 < from + w) {
+        const int64_t u = u0 - from;
+        int lo = 0, hi = r.n_tiles - 1;  // the last row tile that starts at or before u
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (steps_before(p, r, mid) <= u) lo = mid; else hi = mid - 1;
+        }
+        const int64_t at = steps_before(p, r, lo);
+        s->b = b0 + tid;
+        s->tile = lo;
+        s->k0 = static_cast<int32_t>(u - at);
+        s->pos = u0;
+        s->end = u1;
+        if (!p.cut && u > at) {  // the row tile belongs to the run it starts in: begin with the next
+          s->k0 = 0;
+          s->pos = from + steps_before(p, r, lo + 1);
+          if (lo + 1 < r.n_tiles) {
+            s->tile = lo + 1;
+          } else if (s->pos < u1) {
+            int b = b0 + tid;
+            do ++b; while (load_request(p, b).n_tiles == 0);
+            s->b = b;
+            s->tile = 0;
+          }
+        }
+      }
+      base += all;
+    }
+  }
+  fence_proxy_async_smem();  // the copies that follow write where the scratch was
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_constant__ DenseParams p,
+                                                                const __grid_constant__ CUtensorMap qmap,
+                                                                const __grid_constant__ CUtensorMap kvmap,
+                                                                const __grid_constant__ CUtensorMap ropemap,
+                                                                const __grid_constant__ CUtensorMap rowmap) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars* s = reinterpret_cast<Bars*>(smem + kSmBar);
+  float* red = reinterpret_cast<float*>(smem + kSmRed);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = static_cast<int>(cluster_ctarank());
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+
+  if (smem_u32(smem) & 1023u) {  // the tiles need it (without static arrays the dynamic part starts there)
+    if (tid == 0) report(p.dev_status, DSA_DEVERR_TIMEOUT);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < 4; ++k) mbar_init(&s->full[i][k], 1);
+      mbar_init(&s->other[i], 1);
+      mbar_init(&s->s_full[i], 1);
+      mbar_init(&s->pv_done[i], 1);
+      mbar_init(&s->rows[i], 4);
+    }
+    mbar_init(&s->rope, 1);
+    mbar_init(&s->q, 1);
+    mbar_init(&s->p_full, 16);
+    fence_mbar_init();
+    s->abort = 0;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc_pair(&s->tmem, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (tid == kKeyWarp * 32) {
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kvmap);
+    prefetch_tmap(&ropemap);
+    prefetch_tmap(&rowmap);
+  }
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers exist
+  tc_fence_after();
+  const uint32_t tmem = s->tmem;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  plan_run(p, s, smem + kSmKv, pair, n_pairs);
+
+  const auto abort_now = [&] {
+    s->abort = 1;
+    report(p.dev_status, DSA_DEVERR_TIMEOUT);
+  };
+  // a barrier's address in the even CTA
+  const auto even = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
+
+  if (warp == kKeyWarp) {
+    // ---------------- the own keys of each step, all 512 latent dims
+    Cursor c;
+    int it = 0;
+    bool ok = true;
+    for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
+      for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
+        const int buf = it & 1;
+        const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + r, lane == 0);
+        if (it >= 2 && !warp_wait(&s->pv_done[buf], ((it >> 1) - 1) & 1)) {
+          if (lane == 0) abort_now();
+          ok = false;
+          break;
+        }
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          if (r == 0 && lane == 0) mbar_arrive_expect_tx(&s->full[buf][k], 2 * kSlot);
+          load_keys(smem_u32(smem + kSmKv + (buf * 4 + k) * kSlot), &kvmap, &rowmap, even(&s->full[buf][k]), x,
+                    p.total_rows, 2 * k, 2, lane);
+        }
+      }
+    }
+  } else if (warp == kAuxWarp) {
+    // ---------------- after S of a step: the rope dims of the next step's own
+    // keys (and q, when a row tile begins), then this step's other keys
+    Cursor c;
+    int it = 0;
+    Rows other{0, 0};
+    const auto after_s = [&](int i) {  // S of step i is complete: its other keys replace the dims of the other CTA
+      const int buf = i & 1;
+      if (r == 0 && lane == 0) mbar_arrive_expect_tx(&s->other[buf], 4 * kSlot);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k)
+        load_keys(smem_u32(smem + kSmKv + (buf * 4 + 2 * (r ^ 1) + k) * kSlot), &kvmap, &rowmap, even(&s->other[buf]),
+                  other, p.total_rows, 2 * (2 * r + k), 2, lane);
+    };
+    bool ok = true;
+    for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
+      for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
+        const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + r, false);
+        const Rows next_other = rows_of(p, c.b, c.req.kv_len, 2 * kt + (r ^ 1), false);
+        if (it >= 1 && !warp_wait(&s->s_full[(it - 1) & 1], ((it - 1) >> 1) & 1)) {
+          if (lane == 0) abort_now();
+          ok = false;
+          break;
+        }
+        if (r == 0 && lane == 0) mbar_arrive_expect_tx(&s->rope, 2 * 8192);
+        load_keys(smem_u32(smem + kSmRope), &ropemap, &rowmap, even(&s->rope), x, p.total_rows, 8, 1, lane);
+        if (it >= 1) after_s(it - 1);
+        if (kt == c.k0 && lane == 0) {
+          if (r == 0) mbar_arrive_expect_tx(&s->q, 2 * 9 * 8192);
+          const int row0 = (c.req.q0 + c.tile * p.tpt) * p.H + 64 * r;
+          tma_load_3d_pair(smem_u32(smem + kSmQ), &qmap, even(&s->q), 0, row0, 0);
+        }
+        __syncwarp();
+        other = next_other;
+      }
+    }
+    if (ok && it >= 1) {
+      if (warp_wait(&s->s_full[(it - 1) & 1], ((it - 1) >> 1) & 1)) after_s(it - 1);
+      else if (lane == 0) abort_now();
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else if (warp == kMmaWarp) {
+    // ---------------- MMA: one thread of the even CTA issues for the pair
+    // whatever is ready, PV of the oldest step first
+    if (r == 0 && lane == 0) {
+      const uint32_t idesc_qk = idesc_bf16(128, kTile, false, false);
+      const uint32_t idesc_pv = idesc_bf16(128, 256, false, true);
+      const uint64_t dq = smem_desc(smem_u32(smem + kSmQ), 16, 1024, kSwizzle128B);
+      const uint64_t dkv = smem_desc(smem_u32(smem + kSmKv), 16, 1024, kSwizzle128B);
+      const uint64_t drope = smem_desc(smem_u32(smem + kSmRope), 16, 1024, kSwizzle128B);
+      const uint64_t dp = smem_desc(smem_u32(smem + kSmP), 16, 1024, kSwizzle128B);
+      const uint64_t dv = smem_desc(smem_u32(smem + kSmKv), 8192, 1024, kSwizzle128B);
+      Cursor cq, cp;
+      bool more_q = cq.start(p, s), more_p = cp.start(p, s);
+      int iq = 0, ip = 0, sub = 0, segs = 0;  // the next S (and its part) and PV
+      int kq = cq.k0, kp = cp.k0;
+      long long idle_since = clock64();
+      while (more_p && !s->abort) {
+        bool progressed = false;
+        if (ip < iq && mbar_test_wait_cluster(&s->p_full, ip & 1) && mbar_test_wait(&s->other[ip & 1], (ip >> 1) & 1)) {
+          tc_fence_after();
+          const int buf = ip & 1;
+#pragma unroll 1
+          for (int ks = 0; ks < 8; ++ks) {  // 16 keys each
+            const uint64_t a = dp + static_cast<uint64_t>(((ks >> 2) * 8192 + (ks & 3) * 32) >> 4);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint64_t b =
+                  dv + static_cast<uint64_t>(((buf * 4 + 2 * (ks >> 2) + j) * kSlot + (ks & 3) * 2048) >> 4);
+              mma_bf16_ss_pair(tmem + kColO + 128 * j, a, b, idesc_pv, (kp > cp.k0 || ks > 0) ? 1u : 0u);
+            }
+          }
+          mma_commit_pair(&s->pv_done[buf]);
+          ++ip;
+          if (++kp == cp.k1) {
+            more_p = cp.next(p);
+            kp = cp.k0;
+          }
+          progressed = true;
+        }
+        if (more_q && iq < ip + 2) {  // PV of step iq - 2 has been issued: S was read
+          const int buf = iq & 1;
+          bool ready = sub < 4 ? mbar_test_wait(&s->full[buf][sub], (iq >> 1) & 1) : mbar_test_wait(&s->rope, iq & 1);
+          if (ready && sub == 0 && kq == cq.k0) ready = mbar_test_wait(&s->q, segs & 1);
+          if (ready) {
+            tc_fence_after();
+            const uint32_t d = tmem + kColS + 64 * buf;
+            if (sub < 4) {
+#pragma unroll 1
+              for (int st = 0; st < 8; ++st)
+                mma_bf16_ss_pair(d, dq + static_cast<uint64_t>(((2 * sub + (st >> 2)) * 8192 + (st & 3) * 32) >> 4),
+                                 dkv + static_cast<uint64_t>(((buf * 4 + sub) * kSlot + (st >> 2) * 8192 + (st & 3) * 32) >> 4),
+                                 idesc_qk, (sub | st) ? 1u : 0u);
+              ++sub;
+            } else {
+#pragma unroll 1
+              for (int st = 0; st < 4; ++st)
+                mma_bf16_ss_pair(d, dq + static_cast<uint64_t>((8 * 8192 + st * 32) >> 4),
+                                 drope + static_cast<uint64_t>((st * 32) >> 4), idesc_qk, 1u);
+              mma_commit_pair(&s->s_full[buf]);
+              sub = 0;
+              ++iq;
+              if (++kq == cq.k1) {
+                ++segs;
+                more_q = cq.next(p);
+                kq = cq.k0;
+              }
+            }
+            progressed = true;
+          }
+        }
+        if (progressed) idle_since = clock64();
+        else if (clock64() - idle_since > kWaitLimitCycles) abort_now();
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax: TMEM lane = 32 (warp % 4) + lane holds row
+    // lane % 64 against the keys of CTA lane / 64; the two warps of a lane
+    // group take 32 keys (and 128 columns of O) each
+    const int l128 = (warp & 3) * 32 + lane, row = l128 & 63, kh = l128 >> 6, half = warp >> 2;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t p_full = even(&s->p_full);
+    uint8_t* p_dst = smem + kSmP + kh * 8192;
+    Cursor c;
+    int it = 0;
+    uint32_t meets = 0;
+    bool ok = true;
+    // the four warps that hold the same 32 rows: what each wrote is seen by all
+    const auto meet = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s->rows[warp & 1]);
+      return warp_wait(&s->rows[warp & 1], meets++ & 1);
+    };
+    for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
+      const int in_tile = 64 * r + row;  // row of the row tile
+      const int tok = c.tile * p.tpt + in_tile / p.H;
+      const bool live = in_tile < p.tpt * p.H && tok < c.req.q_len;
+      const int lim = live ? visible(c.req, tok) : 0;
+      float m = kNegSentinel, l = 0.f;
+      for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
+        const int buf = it & 1;
+        const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + kh, false);
+        const int n = x.n == 0 ? 0 : lim - kt * kTile - kh * 64 - half * 32;  // of this thread's 32 keys, visible ones
+        if (!warp_wait(&s->s_full[buf], (it >> 1) & 1)) {
+          if (lane == 0) abort_now();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float sc[32];
+        {
+          uint32_t v[32];
+          tmem_ld32_sync(lane_base + kColS + 64 * buf + 32 * half, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sc[i] = __uint_as_float(v[i]) * p.scale_log2;
+        }
+        if (n < 32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sc[i] = i < n ? sc[i] : -INFINITY;
+        }
+        float mt = sc[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) mt = fmaxf(mt, sc[i]);
+        float* rd = red + buf * 256;
+        rd[(2 * half + kh) * 64 + row] = mt;
+        if (!meet()) {
+          if (lane == 0) abort_now();
+          ok = false;
+          break;
+        }
+        mt = fmaxf(fmaxf(rd[row], rd[64 + row]), fmaxf(rd[128 + row], rd[192 + row]));
+        const bool rescale = mt > m + kRescaleThreshold;
+        const float m_new = rescale ? mt : m, neg_m = -m_new;
+        float s0 = 0.f, s1 = 0.f;
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          // the sum takes the fp32 weights; the product takes them rounded to bf16
+          const float a = ex2_approx(sc[2 * i] + neg_m), b = ex2_approx(sc[2 * i + 1] + neg_m);
+          s0 += a;
+          s1 += b;
+          pk[i] = pack_bf16(a, b);
+        }
+        const float alpha = rescale ? ex2_approx(m - m_new) : 1.f;
+        l = l * alpha + (s0 + s1);
+        m = m_new;
+        // P and O are free once PV of the step before is done
+        if (it >= 1 && !warp_wait(&s->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1)) {
+          if (lane == 0) abort_now();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(p_dst + sw128_offset(row, 4 * half + i)) =
+              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        if (kt > c.k0 && __any_sync(0xFFFFFFFFu, rescale)) {
+#pragma unroll 1
+          for (int q = 0; q < 128; q += 32) {
+            uint32_t o[32];
+            tmem_ld32_sync(lane_base + kColO + 128 * half + q, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(lane_base + kColO + 128 * half + q, o);
+          }
+          tmem_st_wait();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_full);
+      }
+      if (!ok) break;
+      // ---- the row tile's (or its part's) result
+      float* sums = red + (it & 1) * 256;  // the maxima of the step before the last: read by all
+      sums[(2 * half + kh) * 64 + row] = l;
+      ok = meet();
+      l = sums[row] + sums[64 + row] + sums[128 + row] + sums[192 + row];
+      ok = ok && meet() && warp_wait(&s->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+      if (!ok) {
+        if (lane == 0) abort_now();
+        break;
+      }
+      tc_fence_after();
+      const uint32_t o_base = lane_base + kColO + 128 * half;
+      if (c.k0 == 0 && c.k1 == c.nk) {
+        const int64_t grow = static_cast<int64_t>(c.req.q0 + c.tile * p.tpt) * p.H + in_tile;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        uint16_t* dst = p.out + grow * kDv + 256 * kh + 128 * half;
+#pragma unroll 1
+        for (int q = 0; q < 128; q += 32) {
+          uint32_t o[32];
+          tmem_ld32_sync(o_base + q, o);
+#pragma unroll
+          for (int e = 0; e < 2 && live; ++e) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[i] = pack_bf16(__uint_as_float(o[16 * e + 2 * i]) * inv, __uint_as_float(o[16 * e + 2 * i + 1]) * inv);
+            uint16_t* d = dst + q + 16 * e;
+            if (p.out32) {
+              st_global_v8(d, w);
+            } else {
+              reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+          __syncwarp();
+        }
+        if (live && kh == 0 && half == 0 && p.lse != nullptr)
+          p.lse[grow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      } else {
+        const int slot = 2 * pair + (c.k0 > 0 ? 0 : 1);
+        float4* dst = p.o_part + (static_cast<int64_t>(2 * slot + r) * 64 + 32 * half) * 128 + l128;
+#pragma unroll 1
+        for (int q = 0; q < 128; q += 32) {
+          uint32_t o[32];
+          tmem_ld32_sync(o_base + q, o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[(q / 4 + i) * 128] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        }
+        if (kh == 0 && half == 0) p.ml_part[slot * 128 + in_tile] = make_float2(m, l);
+        if (c.k0 == 0 && r == 0 && tid == 0) {
+          // pairs whose runs hold the rest of this row tile
+          const int last = static_cast<int>((c.pos + c.nk - 1) / s->per);
+          const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt) - c.tile * p.tpt) * p.H;
+          p.desc[pair] = make_int4((c.req.q0 + c.tile * p.tpt) * p.H, rows, last - pair, 0);
+        }
+      }
+      tc_fence_before();
+    }
+    if (p.cut && r == 0 && tid == 0 && ok) {
+      // nothing to join: no row tile that starts in this run goes on behind it
+      if (s->pos >= s->end || c.k0 > 0 || c.k1 == c.nk) p.desc[pair] = make_int4(0, 0, 0, 0);
+    }
+    if (p.cut && r == 0 && tid == 0 && !ok) p.desc[pair] = make_int4(0, 0, 0, 0);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (s->abort) {
+    // a wait ran out: let copies and MMAs in flight end before the memory they use is given up
+    const long long t0 = clock64();
+    while (clock64() - t0 < 20000000ll) __nanosleep(1000);
+  }
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// Joins the partials of the row tile that starts in pair blockIdx.y's run and
+// goes on behind it: out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j. A
+// thread takes 16 dims of a row, one 32-byte sector of the result.
+__global__ void __launch_bounds__(128) dense_mla_merge_kernel(const __grid_constant__ DenseParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int pair = blockIdx.y;
+  const int4 d = p.desc[pair];
+  if (d.z <= 0) return;
+  const int r = blockIdx.x >> 4, g = blockIdx.x & 15;  // CTA, 4 column groups
+  const int lane = threadIdx.x, in_tile = 64 * r + (lane & 63);
+  if (in_tile >= d.y) return;
+  const int parts = d.z + 1;
+  const auto slot = [&](int j) { return j == 0 ? 2 * pair + 1 : 2 * (pair + j); };
+  float M = kNegSentinel;
+  for (int j = 0; j < parts; ++j) M = fmaxf(M, p.ml_part[slot(j) * 128 + in_tile].x);
+  float den = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < parts; ++j) {
+    const float2 ml = p.ml_part[slot(j) * 128 + in_tile];
+    const float w = exp2f(ml.x - M);
+    den = fmaf(w, ml.y, den);
+    const float4* o = p.o_part + (static_cast<int64_t>(2 * slot(j) + r) * 64 + 4 * g) * 128 + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = o[i * 128];
+      acc[i].x = fmaf(w, v.x, acc[i].x);
+      acc[i].y = fmaf(w, v.y, acc[i].y);
+      acc[i].z = fmaf(w, v.z, acc[i].z);
+      acc[i].w = fmaf(w, v.w, acc[i].w);
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const int64_t row = static_cast<int64_t>(d.x) + in_tile;
+  uint4* dst = reinterpret_cast<uint4*>(p.out + row * kDv + 256 * (lane >> 6) + 16 * g);
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    dst[e] = make_uint4(pack_bf16(acc[2 * e].x * inv, acc[2 * e].y * inv), pack_bf16(acc[2 * e].z * inv, acc[2 * e].w * inv),
+                        pack_bf16(acc[2 * e + 1].x * inv, acc[2 * e + 1].y * inv),
+                        pack_bf16(acc[2 * e + 1].z * inv, acc[2 * e + 1].w * inv));
+  if (g == 0 && lane < 64 && p.lse != nullptr) p.lse[row] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
+}
+
+FuncAttrOnce g_smem_dense, g_smem_dense_merge;
+
+int num_pairs() { return std::max(1, num_sms() / 2); }
+size_t o_part_bytes(int pairs) { return static_cast<size_t>(2 * pairs) * 128 * kDv * sizeof(float); }
+size_t ml_part_bytes(int pairs) { return static_cast<size_t>(2 * pairs) * 128 * sizeof(float2); }
+size_t workspace_bytes(int pairs) { return o_part_bytes(pairs) + ml_part_bytes(pairs) + pairs * sizeof(int4); }
+
+dsa_status_t launch_dense(const DenseParams& p, const void* q, const void* kv, int pairs, cudaStream_t s) {
+  CUtensorMap qmap, kvmap, ropemap, rowmap;
+  const uint64_t rows = static_cast<uint64_t>(p.total_rows);
+  // rows of 9 blocks of 64 dims, as a block-major box
+  const uint64_t strides[2] = {kDk * 2, 128};
+  const uint64_t qdims[3] = {64, static_cast<uint64_t>(p.T) * p.H, 9}, kvdims[3] = {64, rows, 9};
+  const uint32_t qbox[3] = {64, 64, 9}, kvbox[3] = {64, 64, 2}, ropebox[3] = {64, 64, 1}, rowbox[2] = {64, 1};
+  const uint64_t rowdims[2] = {kDk, rows};
+  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  dsa_status_t st;
+  if ((st = make_tmap(&qmap, bf16, 3, q, qdims, strides, qbox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&kvmap, bf16, 3, kv, kvdims, strides, kvbox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&ropemap, bf16, 3, kv, kvdims, strides, ropebox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&rowmap, bf16, 2, kv, rowdims, strides, rowbox, sw)) != DSA_OK) return st;
+  if ((st = allow_smem(dense_mla_kernel, kSmTotal, g_smem_dense)) != DSA_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmTotal;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_kernel, p, qmap, kvmap, ropemap, rowmap);
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_kernel launch failed: %s", cudaGetErrorString(e));
+  if (p.cut) {
+    if ((st = allow_smem(dense_mla_merge_kernel, 0, g_smem_dense_merge)) != DSA_OK) return st;
+    cfg.gridDim = dim3(32, static_cast<unsigned>(pairs));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, dense_mla_merge_kernel, p);
+    if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_merge_kernel launch failed: %s", cudaGetErrorString(e));
+  }
+  return check_launch("dense_mla_kernel");
+}
+
+// ---------------------------------------------------------------------------
+// fp8 cache, the simple form: one warp per (token, head), the 8 warps of a CTA
+// taking 8 heads of a token; a lane holds dims {2 lane + 64 i, 2 lane + 64 i +
+// 1} of q and of the output, and the softmax runs over the keys one at a time.
+struct SimpleParams {
   const uint16_t* q;
   const uint8_t* kv;
   int64_t block_bytes;
@@ -38,7 +808,7 @@ struct DenseParams {
 };
 
 template <bool F8>
-__global__ void __launch_bounds__(256) dense_mla_simple_kernel(const __grid_constant__ DenseParams p) {
+__global__ void __launch_bounds__(256) dense_mla_simple_kernel(const __grid_constant__ SimpleParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x, h = blockIdx.y * 8 + warp;
   if (h >= p.H || t >= __ldg(p.qsl + p.B)) return;
@@ -133,6 +903,8 @@ dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_st
     return fail(DSA_ERR_INVALID_ARG, "%s: num_kv_splits %d not in {-1, 0, 1}", name, num_kv_splits);
   if (T > 0 && B == 0) return fail(DSA_ERR_INVALID_ARG, "%s: T > 0 with B == 0", name);
   if (T == 0) return DSA_OK;
+  if (static_cast<int64_t>(T) * H >= (int64_t(1) << 31))
+    return fail(DSA_ERR_UNSUPPORTED, "%s: 2^31 query rows or more", name);
   if (!q || !kv_cache || !block_table || !seq_lens || !query_start_loc || !out)
     return fail(DSA_ERR_INVALID_ARG, "%s: null pointer", name);
   if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out))
@@ -151,7 +923,37 @@ dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_st
   const size_t need = dense_mla_workspace_size(T, H, Dv, num_kv_splits);
   if (need && (workspace == nullptr || ws_bytes < need || !aligned16(workspace)))
     return fail(DSA_ERR_WORKSPACE, "%s: needs %zu workspace bytes (16-byte aligned), got %zu", name, need, ws_bytes);
-  DenseParams p;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!f8) {
+    const int pairs = num_pairs();
+    DenseParams d = {};
+    d.num_blocks = num_blocks;
+    d.rows_per_block = static_cast<int32_t>(kv_block_stride / row);
+    d.total_rows = static_cast<int32_t>(std::max<int64_t>(num_blocks * (kv_block_stride / row), 1));
+    d.block_table = block_table;
+    d.bt_stride = bt_stride;
+    d.seq_lens = seq_lens;
+    d.qsl = query_start_loc;
+    d.B = B;
+    d.T = T;
+    d.H = H;
+    d.tpt = 128 / H;
+    d.block_size = block_size;
+    d.bs64 = block_size / 64;
+    d.scale_log2 = softmax_scale * kLog2e;
+    d.cut = num_kv_splits == 0;
+    d.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+    d.out = static_cast<uint16_t*>(out);
+    d.lse = lse;
+    if (d.cut) {
+      d.o_part = static_cast<float4*>(workspace);
+      d.ml_part = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + o_part_bytes(pairs));
+      d.desc = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(d.ml_part) + ml_part_bytes(pairs));
+    }
+    d.dev_status = dev_status;
+    return launch_dense(d, q, kv_cache, pairs, s);
+  }
+  SimpleParams p;
   p.q = static_cast<const uint16_t*>(q);
   p.kv = static_cast<const uint8_t*>(kv_cache);
   p.block_bytes = f8 ? kv_block_stride : 2 * kv_block_stride;
@@ -169,9 +971,7 @@ dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_st
   p.lse = lse;
   p.dev_status = dev_status;
   const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>((H + 7) / 8));
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (f8) dense_mla_simple_kernel<true><<<grid, 256, 0, s>>>(p);
-  else dense_mla_simple_kernel<false><<<grid, 256, 0, s>>>(p);
+  dense_mla_simple_kernel<true><<<grid, 256, 0, s>>>(p);
   return check_launch("dense_mla_simple_kernel");
 }
 
@@ -181,8 +981,8 @@ dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_st
 using namespace dsa;
 
 extern "C" size_t dense_mla_workspace_size(int32_t T, int32_t H, int32_t Dv, int32_t num_kv_splits) {
-  (void)T, (void)H, (void)Dv, (void)num_kv_splits;
-  return 0;
+  if (T <= 0 || H <= 0 || Dv <= 0 || num_kv_splits != 0) return 0;
+  return dsa::workspace_bytes(dsa::num_pairs());
 }
 
 extern "C" dsa_status_t dense_mla_attention(const void* q, const void* kv_cache, int64_t kv_block_stride,
