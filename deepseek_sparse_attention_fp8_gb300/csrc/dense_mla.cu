@@ -60,10 +60,12 @@ static_assert(kSmTotal <= 232448, "more than 227 KB of shared memory");
 
 struct Bars {
   uint64_t full[2][4];   // a slot's own keys, of both CTAs (the even CTA's barrier)
-  uint64_t other[2];     // a step's other keys, of both CTAs (the even CTA's)
+  uint64_t other[2][2];  // a step's other keys: those of CTA r, for CTA r ^ 1 (the even CTA's)
   uint64_t rope, q;      // (the even CTA's)
   uint64_t p_full;       // P written by the 16 softmax warps of the pair (the even CTA's)
+  uint64_t s_half[2];    // the first two slots of a step have entered S (in both CTAs)
   uint64_t s_full[2];    // S of a step complete (in both CTAs)
+  uint64_t pv_half[2];   // the first 64 keys of a step have entered O (in both CTAs)
   uint64_t pv_done[2];   // O += P V of a step complete (in both CTAs)
   uint64_t rows[2];      // the four softmax warps that share 32 rows
   uint32_t tmem;
@@ -342,7 +344,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       for (int k = 0; k < 4; ++k) mbar_init(&s->full[i][k], 1);
-      mbar_init(&s->other[i], 1);
+      mbar_init(&s->other[i][0], 1);
+      mbar_init(&s->other[i][1], 1);
+      mbar_init(&s->s_half[i], 1);
+      mbar_init(&s->pv_half[i], 1);
       mbar_init(&s->s_full[i], 1);
       mbar_init(&s->pv_done[i], 1);
       mbar_init(&s->rows[i], 4);
@@ -386,46 +391,58 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
       for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
         const int buf = it & 1;
         const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + r, lane == 0);
-        if (it >= 2 && !warp_wait(&s->pv_done[buf], ((it >> 1) - 1) & 1)) {
-          if (lane == 0) abort_now();
-          ok = false;
-          break;
-        }
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
+          if (it >= 2 && (k & 1) == 0 && !warp_wait(k == 0 ? &s->pv_half[buf] : &s->pv_done[buf], ((it >> 1) - 1) & 1)) {
+            if (lane == 0) abort_now();
+            ok = false;
+            break;
+          }
           if (r == 0 && lane == 0) mbar_arrive_expect_tx(&s->full[buf][k], 2 * kSlot);
           load_keys(smem_u32(smem + kSmKv + (buf * 4 + k) * kSlot), &kvmap, &rowmap, even(&s->full[buf][k]), x,
                     p.total_rows, 2 * k, 2, lane);
         }
+        if (!ok) break;
       }
     }
   } else if (warp == kAuxWarp) {
-    // ---------------- after S of a step: the rope dims of the next step's own
-    // keys (and q, when a row tile begins), then this step's other keys
+    // ---------------- each step's other keys, as soon as S no longer needs
+    // the dims they replace (CTA 1: after the first two slots, CTA 0: after
+    // all), the rope dims of the next step's own keys, and q when a row tile
+    // begins
     Cursor c;
     int it = 0;
     Rows other{0, 0};
-    const auto after_s = [&](int i) {  // S of step i is complete: its other keys replace the dims of the other CTA
+    const auto load_other = [&](int i) {
       const int buf = i & 1;
-      if (r == 0 && lane == 0) mbar_arrive_expect_tx(&s->other[buf], 4 * kSlot);
+      if (r == 0 && lane == 0) {
+        mbar_arrive_expect_tx(&s->other[buf][0], 2 * kSlot);
+        mbar_arrive_expect_tx(&s->other[buf][1], 2 * kSlot);
+      }
 #pragma unroll 1
       for (int k = 0; k < 2; ++k)
-        load_keys(smem_u32(smem + kSmKv + (buf * 4 + 2 * (r ^ 1) + k) * kSlot), &kvmap, &rowmap, even(&s->other[buf]),
-                  other, p.total_rows, 2 * (2 * r + k), 2, lane);
+        load_keys(smem_u32(smem + kSmKv + (buf * 4 + 2 * (r ^ 1) + k) * kSlot), &kvmap, &rowmap,
+                  even(&s->other[buf][r ^ 1]), other, p.total_rows, 2 * (2 * r + k), 2, lane);
     };
     bool ok = true;
+    const auto after_s = [&](int i) {  // what follows S of step i; false when a wait ran out
+      const int ph = (i >> 1) & 1;
+      if (r == 1) {
+        ok = warp_wait(&s->s_half[i & 1], ph);
+        if (ok) load_other(i);
+      }
+      ok = ok && warp_wait(&s->s_full[i & 1], ph);
+      if (!ok && lane == 0) abort_now();
+      return ok;
+    };
     for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
       for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
         const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + r, false);
         const Rows next_other = rows_of(p, c.b, c.req.kv_len, 2 * kt + (r ^ 1), false);
-        if (it >= 1 && !warp_wait(&s->s_full[(it - 1) & 1], ((it - 1) >> 1) & 1)) {
-          if (lane == 0) abort_now();
-          ok = false;
-          break;
-        }
+        if (it >= 1 && !after_s(it - 1)) break;
         if (r == 0 && lane == 0) mbar_arrive_expect_tx(&s->rope, 2 * 8192);
         load_keys(smem_u32(smem + kSmRope), &ropemap, &rowmap, even(&s->rope), x, p.total_rows, 8, 1, lane);
-        if (it >= 1) after_s(it - 1);
+        if (it >= 1 && r == 0) load_other(it - 1);
         if (kt == c.k0 && lane == 0) {
           if (r == 0) mbar_arrive_expect_tx(&s->q, 2 * 9 * 8192);
           const int row0 = (c.req.q0 + c.tile * p.tpt) * p.H + 64 * r;
@@ -435,70 +452,84 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
         other = next_other;
       }
     }
-    if (ok && it >= 1) {
-      if (warp_wait(&s->s_full[(it - 1) & 1], ((it - 1) >> 1) & 1)) after_s(it - 1);
-      else if (lane == 0) abort_now();
-    }
+    if (ok && it >= 1 && after_s(it - 1) && r == 0) load_other(it - 1);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   } else if (warp == kMmaWarp) {
-    // ---------------- MMA: one thread of the even CTA issues for the pair
-    // whatever is ready, PV of the oldest step first
-    if (r == 0 && lane == 0) {
+    // ---------------- MMA: the even CTA issues for the pair whatever is
+    // ready, PV of the oldest step first. The warp stays converged, so that the
+    // descriptors live in uniform registers, and one lane issues.
+    if (r == 0) {
       const uint32_t idesc_qk = idesc_bf16(128, kTile, false, false);
       const uint32_t idesc_pv = idesc_bf16(128, 256, false, true);
-      const uint64_t dq = smem_desc(smem_u32(smem + kSmQ), 16, 1024, kSwizzle128B);
-      const uint64_t dkv = smem_desc(smem_u32(smem + kSmKv), 16, 1024, kSwizzle128B);
-      const uint64_t drope = smem_desc(smem_u32(smem + kSmRope), 16, 1024, kSwizzle128B);
-      const uint64_t dp = smem_desc(smem_u32(smem + kSmP), 16, 1024, kSwizzle128B);
-      const uint64_t dv = smem_desc(smem_u32(smem + kSmKv), 8192, 1024, kSwizzle128B);
+      // K-major tiles (q, keys, P): 8-row groups 1024 bytes apart; keys as
+      // values (dims along N): 64-dim blocks 8192 bytes apart
+      const uint64_t dk = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      const uint64_t dv = smem_desc(smem_u32(smem), 8192, 1024, kSwizzle128B);
+      const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
+      const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
       Cursor cq, cp;
       bool more_q = cq.start(p, s), more_p = cp.start(p, s);
-      int iq = 0, ip = 0, sub = 0, segs = 0;  // the next S (and its part) and PV
+      int iq = 0, ip = 0, sub = 0, half = 0, segs = 0;  // the next S and PV, and the parts of them
       int kq = cq.k0, kp = cp.k0;
+      const auto all = [](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
       long long idle_since = clock64();
-      while (more_p && !s->abort) {
+      while (more_p && !__any_sync(0xFFFFFFFFu, s->abort)) {
         bool progressed = false;
-        if (ip < iq && mbar_test_wait_cluster(&s->p_full, ip & 1) && mbar_test_wait(&s->other[ip & 1], (ip >> 1) & 1)) {
+        if (ip < iq && all(half == 0 ? mbar_test_wait(&s->p_full, ip & 1) && mbar_test_wait(&s->other[ip & 1][0], (ip >> 1) & 1)
+                                     : mbar_test_wait(&s->other[ip & 1][1], (ip >> 1) & 1))) {
           tc_fence_after();
           const int buf = ip & 1;
-#pragma unroll 1
-          for (int ks = 0; ks < 8; ++ks) {  // 16 keys each
-            const uint64_t a = dp + static_cast<uint64_t>(((ks >> 2) * 8192 + (ks & 3) * 32) >> 4);
+          const uint32_t a0 = k_lo + ((kSmP + half * 8192) >> 4);
+          const uint32_t b0 = v_lo + ((kSmKv + (buf * 4 + 2 * half) * kSlot) >> 4);
+          const uint32_t acc0 = (kp > cp.k0 || half) ? 1u : 0u;
+          if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint64_t b =
-                  dv + static_cast<uint64_t>(((buf * 4 + 2 * (ks >> 2) + j) * kSlot + (ks & 3) * 2048) >> 4);
-              mma_bf16_ss_pair(tmem + kColO + 128 * j, a, b, idesc_pv, (kp > cp.k0 || ks > 0) ? 1u : 0u);
+            for (int ks = 0; ks < 4; ++ks) {  // 16 keys each
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma_bf16_ss_pair(tmem + kColO + 128 * j, a0 + ((ks * 32) >> 4), k_hi,
+                                 b0 + ((j * kSlot + ks * 2048) >> 4), v_hi, idesc_pv, ks > 0 ? 1u : acc0);
+            }
+            mma_commit_pair(half ? &s->pv_done[buf] : &s->pv_half[buf]);
+          }
+          __syncwarp();
+          if (half) {
+            ++ip;
+            if (++kp == cp.k1) {
+              more_p = cp.next(p);
+              kp = cp.k0;
             }
           }
-          mma_commit_pair(&s->pv_done[buf]);
-          ++ip;
-          if (++kp == cp.k1) {
-            more_p = cp.next(p);
-            kp = cp.k0;
-          }
+          half ^= 1;
           progressed = true;
         }
         if (more_q && iq < ip + 2) {  // PV of step iq - 2 has been issued: S was read
           const int buf = iq & 1;
           bool ready = sub < 4 ? mbar_test_wait(&s->full[buf][sub], (iq >> 1) & 1) : mbar_test_wait(&s->rope, iq & 1);
-          if (ready && sub == 0 && kq == cq.k0) ready = mbar_test_wait(&s->q, segs & 1);
-          if (ready) {
+          if (sub == 0 && kq == cq.k0) ready = ready && mbar_test_wait(&s->q, segs & 1);
+          if (all(ready)) {
             tc_fence_after();
             const uint32_t d = tmem + kColS + 64 * buf;
             if (sub < 4) {
-#pragma unroll 1
-              for (int st = 0; st < 8; ++st)
-                mma_bf16_ss_pair(d, dq + static_cast<uint64_t>(((2 * sub + (st >> 2)) * 8192 + (st & 3) * 32) >> 4),
-                                 dkv + static_cast<uint64_t>(((buf * 4 + sub) * kSlot + (st >> 2) * 8192 + (st & 3) * 32) >> 4),
-                                 idesc_qk, (sub | st) ? 1u : 0u);
+              const uint32_t a0 = k_lo + ((kSmQ + sub * 2 * 8192) >> 4);
+              const uint32_t b0 = k_lo + ((kSmKv + (buf * 4 + sub) * kSlot) >> 4);
+              const uint32_t acc0 = sub > 0 ? 1u : 0u;
+              if (elect_one()) {
+#pragma unroll
+                for (int st = 0; st < 8; ++st)
+                  mma_bf16_ss_pair(d, a0 + (((st >> 2) * 8192 + (st & 3) * 32) >> 4), k_hi,
+                                   b0 + (((st >> 2) * 8192 + (st & 3) * 32) >> 4), k_hi, idesc_qk, st > 0 ? 1u : acc0);
+                if (sub == 1) mma_commit_pair(&s->s_half[buf]);
+              }
               ++sub;
             } else {
-#pragma unroll 1
-              for (int st = 0; st < 4; ++st)
-                mma_bf16_ss_pair(d, dq + static_cast<uint64_t>((8 * 8192 + st * 32) >> 4),
-                                 drope + static_cast<uint64_t>((st * 32) >> 4), idesc_qk, 1u);
-              mma_commit_pair(&s->s_full[buf]);
+              if (elect_one()) {
+#pragma unroll
+                for (int st = 0; st < 4; ++st)
+                  mma_bf16_ss_pair(d, k_lo + ((kSmQ + 8 * 8192 + st * 32) >> 4), k_hi,
+                                   k_lo + ((kSmRope + st * 32) >> 4), k_hi, idesc_qk, 1u);
+                mma_commit_pair(&s->s_full[buf]);
+              }
               sub = 0;
               ++iq;
               if (++kq == cq.k1) {
@@ -507,11 +538,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
                 kq = cq.k0;
               }
             }
+            __syncwarp();
             progressed = true;
           }
         }
         if (progressed) idle_since = clock64();
-        else if (clock64() - idle_since > kWaitLimitCycles) abort_now();
+        else if (all(clock64() - idle_since > kWaitLimitCycles) && lane == 0) abort_now();
       }
     }
     __syncwarp();
@@ -521,6 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
     // group take 32 keys (and 128 columns of O) each
     const int l128 = (warp & 3) * 32 + lane, row = l128 & 63, kh = l128 >> 6, half = warp >> 2;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    // P stays in this CTA's shared memory, whose tensor core reads it there:
+    // the proxy fence before the arrival orders the data, and only the arrival
+    // itself crosses to the even CTA. (A release at cluster scope instead took
+    // 1300-2000 clocks per step.)
     const uint32_t p_full = even(&s->p_full);
     uint8_t* p_dst = smem + kSmP + kh * 8192;
     Cursor c;
@@ -611,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(p_full);
+        if (lane == 0) mbar_arrive_remote_relaxed(p_full);
       }
       if (!ok) break;
       // ---- the row tile's (or its part's) result
