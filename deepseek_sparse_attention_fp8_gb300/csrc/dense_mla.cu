@@ -42,8 +42,13 @@ constexpr int kDk = 576, kDv = 512, kF8Row = 656;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-constexpr int kThreads = 352;  // warps 0-7 softmax, 8 keys, 9 q / rope / other keys, 10 MMA
-constexpr int kKeyWarp = 8, kAuxWarp = 9, kMmaWarp = 10;
+// warps 0-7 softmax, 8 q / rope (bf16 cache: and the other keys), 9 MMA, then
+// the own keys: one warp of TMA copies, or (fp8 cache) 8 decoding warps, and 4
+// more for the other keys
+constexpr int kAuxWarp = 8, kMmaWarp = 9, kKeyWarp = 10, kKeyWarpsF8 = 8, kOtherWarpsF8 = 4;
+constexpr int kOtherWarp = kKeyWarp + kKeyWarpsF8;  // fp8 only
+template <bool F8>
+constexpr int kThreadsOf = 32 * (F8 ? kOtherWarp + kOtherWarpsF8 : kKeyWarp + 1);
 constexpr int kTile = 128;
 constexpr int kSlot = 16384;  // 64 keys x 128 dims
 constexpr float kRescaleThreshold = 8.f;  // log2 units
@@ -59,10 +64,10 @@ constexpr int kSmQ = 0, kSmKv = kSmQ + 9 * 8192, kSmRope = kSmKv + 8 * kSlot, kS
 static_assert(kSmTotal <= 232448, "more than 227 KB of shared memory");
 
 struct Bars {
-  uint64_t full[2][4];   // a slot's own keys, of both CTAs (the even CTA's barrier)
-  uint64_t other[2][2];  // a step's other keys: those of CTA r, for CTA r ^ 1 (the even CTA's)
-  uint64_t rope, q;      // (the even CTA's)
-  uint64_t p_full;       // P written by the 16 softmax warps of the pair (the even CTA's)
+  // the first three are the even CTA's barriers, for both CTAs
+  uint64_t full[2][4];   // a slot's own keys, of both CTAs
+  uint64_t other[2][2];  // a step's other keys: those of CTA r, for CTA r ^ 1
+  uint64_t rope, q, p_full;  // the two TMA copies; P written by the 16 softmax warps of the pair
   uint64_t s_half[2];    // the first two slots of a step have entered S (in both CTAs)
   uint64_t s_full[2];    // S of a step complete (in both CTAs)
   uint64_t pv_half[2];   // the first 64 keys of a step have entered O (in both CTAs)
@@ -84,6 +89,7 @@ struct DenseParams {
   int32_t B, T, H, tpt;      // tpt: tokens per row tile
   int32_t block_size, bs64;  // bs64 = block_size / 64
   float scale_log2;
+  const uint8_t* kv;  // the fp8 cache
   int32_t cut;    // row tiles may be cut
   int32_t out32;  // out is 32-byte aligned
   uint16_t* out;
@@ -241,8 +247,31 @@ __device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* box, 
   __syncwarp();
 }
 
+// ---- fp8 cache: a row's 128 codes of one group are 8 lanes' 16 bytes, read
+// straight into registers, decoded (code * scale in fp32, rounded to bf16:
+// the tensor cores take bf16) and stored as the swizzled tile the copies of
+// the bf16 cache would bring.
+__device__ __forceinline__ uint32_t decode2(uint32_t two, float sc) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16(f.x * sc, f.y * sc);
+}
+__device__ __forceinline__ void decode16(uint8_t* slot, int key, int lane8, const uint4& c, float sc) {
+  uint8_t* blk = slot + (lane8 >> 2) * 8192;
+  const uint4 v[2] = {make_uint4(decode2(c.x, sc), decode2(c.x >> 16, sc), decode2(c.y, sc), decode2(c.y >> 16, sc)),
+                      make_uint4(decode2(c.z, sc), decode2(c.z >> 16, sc), decode2(c.w, sc), decode2(c.w >> 16, sc))};
+  // the upper four lanes of a key write another 64-dim block, in the same
+  // banks: they take their two chunks in the other order
+  const bool sw = lane8 & 4;
+  const uint32_t c0 = 2 * (lane8 & 3);
+  *reinterpret_cast<uint4*>(blk + sw128_offset(key, c0 + sw)) = sw ? v[1] : v[0];
+  *reinterpret_cast<uint4*>(blk + sw128_offset(key, c0 + !sw)) = sw ? v[0] : v[1];
+}
+
 // The run of this pair: every CTA sums the requests' steps itself. `scratch`
 // is shared memory that nothing else uses yet.
+template <int kThreads>
 __device__ __forceinline__ void plan_run(const DenseParams& p, Bars* s, uint8_t* scratch, int pair, int n_pairs) {
   int64_t* sums = reinterpret_cast<int64_t*>(scratch);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -325,7 +354,8 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Bars* s, uint8_t*
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_constant__ DenseParams p,
+template <bool F8>
+__global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __grid_constant__ DenseParams p,
                                                                 const __grid_constant__ CUtensorMap qmap,
                                                                 const __grid_constant__ CUtensorMap kvmap,
                                                                 const __grid_constant__ CUtensorMap ropemap,
@@ -343,9 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      for (int k = 0; k < 4; ++k) mbar_init(&s->full[i][k], 1);
-      mbar_init(&s->other[i][0], 1);
-      mbar_init(&s->other[i][1], 1);
+      for (int k = 0; k < 4; ++k) mbar_init(&s->full[i][k], F8 ? 2 * kKeyWarpsF8 : 1);
+      for (int k = 0; k < 2; ++k) mbar_init(&s->other[i][k], F8 ? kOtherWarpsF8 : 1);
       mbar_init(&s->s_half[i], 1);
       mbar_init(&s->pv_half[i], 1);
       mbar_init(&s->s_full[i], 1);
@@ -373,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = s->tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_run(p, s, smem + kSmKv, pair, n_pairs);
+  plan_run<kThreadsOf<F8>>(p, s, smem + kSmKv, pair, n_pairs);
 
   const auto abort_now = [&] {
     s->abort = 1;
@@ -382,7 +411,91 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
   // a barrier's address in the even CTA
   const auto even = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
 
-  if (warp == kKeyWarp) {
+  if (F8 && warp >= kOtherWarp) {
+    // ---------------- fp8: each step's other keys, as soon as S no longer
+    // needs the dims they replace; 16 keys per warp, two groups
+    const int lane8 = lane & 7, key0 = (warp - kOtherWarp) * 16 + (lane >> 3);
+    Cursor c;
+    int it = 0;
+    bool ok = true;
+    for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
+      for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
+        const int buf = it & 1;
+        const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + (r ^ 1), false);
+        uint4 code[4][2];
+        float2 sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          code[i][0] = code[i][1] = make_uint4(0u, 0u, 0u, 0u);
+          sc[i] = make_float2(0.f, 0.f);
+          if (key0 + 4 * i < x.n) {
+            const uint8_t* src = p.kv + static_cast<int64_t>(x.row + key0 + 4 * i) * kF8Row;
+            code[i][0] = __ldg(reinterpret_cast<const uint4*>(src + 256 * r) + lane8);
+            code[i][1] = __ldg(reinterpret_cast<const uint4*>(src + 256 * r + 128) + lane8);
+            sc[i] = __ldg(reinterpret_cast<const float2*>(src + kDv) + r);
+          }
+        }
+        if (!warp_wait(r ? &s->s_half[buf] : &s->s_full[buf], (it >> 1) & 1)) {
+          if (lane == 0) abort_now();
+          ok = false;
+          break;
+        }
+        uint8_t* slot = smem + kSmKv + (buf * 4 + 2 * (r ^ 1)) * kSlot;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          decode16(slot, key0 + 4 * i, lane8, code[i][0], sc[i].x);
+          decode16(slot + kSlot, key0 + 4 * i, lane8, code[i][1], sc[i].y);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(even(&s->other[buf][r ^ 1]));
+      }
+    }
+  } else if (F8 && warp >= kKeyWarp) {
+    // ---------------- fp8: the own keys of each step; 8 keys per warp, loaded
+    // before the step's slots come free
+    const int lane8 = lane & 7, key0 = (warp - kKeyWarp) * 8 + (lane >> 3);
+    Cursor c;
+    int it = 0;
+    bool ok = true;
+    for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
+      for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
+        const int buf = it & 1;
+        const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + r, warp == kKeyWarp && lane == 0);
+        uint4 code[2][4];
+        float4 sc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) code[i][k] = make_uint4(0u, 0u, 0u, 0u);
+          sc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (key0 + 4 * i < x.n) {
+            const uint8_t* src = p.kv + static_cast<int64_t>(x.row + key0 + 4 * i) * kF8Row;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) code[i][k] = __ldg(reinterpret_cast<const uint4*>(src + 128 * k) + lane8);
+            sc[i] = __ldg(reinterpret_cast<const float4*>(src + kDv));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (it >= 2 && (k & 1) == 0 && !warp_wait(k == 0 ? &s->pv_half[buf] : &s->pv_done[buf], ((it >> 1) - 1) & 1)) {
+            if (lane == 0) abort_now();
+            ok = false;
+            break;
+          }
+          uint8_t* slot = smem + kSmKv + (buf * 4 + k) * kSlot;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            decode16(slot, key0 + 4 * i, lane8, code[i][k],
+                     k == 0 ? sc[i].x : k == 1 ? sc[i].y : k == 2 ? sc[i].z : sc[i].w);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_relaxed(even(&s->full[buf][k]));
+        }
+        if (!ok) break;
+      }
+    }
+  } else if (warp == kKeyWarp) {
     // ---------------- the own keys of each step, all 512 latent dims
     Cursor c;
     int it = 0;
@@ -406,10 +519,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
       }
     }
   } else if (warp == kAuxWarp) {
-    // ---------------- each step's other keys, as soon as S no longer needs
-    // the dims they replace (CTA 1: after the first two slots, CTA 0: after
-    // all), the rope dims of the next step's own keys, and q when a row tile
-    // begins
+    // ---------------- each step's other keys (bf16 cache), as soon as S no
+    // longer needs the dims they replace (CTA 1: after the first two slots,
+    // CTA 0: after all), the rope dims of the next step's own keys, and q when
+    // a row tile begins
     Cursor c;
     int it = 0;
     Rows other{0, 0};
@@ -427,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
     bool ok = true;
     const auto after_s = [&](int i) {  // what follows S of step i; false when a wait ran out
       const int ph = (i >> 1) & 1;
-      if (r == 1) {
+      if (!F8 && r == 1) {
         ok = warp_wait(&s->s_half[i & 1], ph);
         if (ok) load_other(i);
       }
@@ -441,8 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
         const Rows next_other = rows_of(p, c.b, c.req.kv_len, 2 * kt + (r ^ 1), false);
         if (it >= 1 && !after_s(it - 1)) break;
         if (r == 0 && lane == 0) mbar_arrive_expect_tx(&s->rope, 2 * 8192);
-        load_keys(smem_u32(smem + kSmRope), &ropemap, &rowmap, even(&s->rope), x, p.total_rows, 8, 1, lane);
-        if (it >= 1 && r == 0) load_other(it - 1);
+        load_keys(smem_u32(smem + kSmRope), &ropemap, &rowmap, even(&s->rope), x, p.total_rows, F8 ? 0 : 8, 1,
+                  lane);
+        if (!F8 && it >= 1 && r == 0) load_other(it - 1);
         if (kt == c.k0 && lane == 0) {
           if (r == 0) mbar_arrive_expect_tx(&s->q, 2 * 9 * 8192);
           const int row0 = (c.req.q0 + c.tile * p.tpt) * p.H + 64 * r;
@@ -452,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_kernel(const __grid_con
         other = next_other;
       }
     }
-    if (ok && it >= 1 && after_s(it - 1) && r == 0) load_other(it - 1);
+    if (!F8 && ok && it >= 1 && after_s(it - 1) && r == 0) load_other(it - 1);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   } else if (warp == kMmaWarp) {
     // ---------------- MMA: the even CTA issues for the pair whatever is
@@ -773,32 +887,36 @@ __global__ void __launch_bounds__(128) dense_mla_merge_kernel(const __grid_const
   if (g == 0 && lane < 64 && p.lse != nullptr) p.lse[row] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
-FuncAttrOnce g_smem_dense, g_smem_dense_merge;
+FuncAttrOnce g_smem_dense[2], g_smem_dense_merge;
 
 int num_pairs() { return std::max(1, num_sms() / 2); }
 size_t o_part_bytes(int pairs) { return static_cast<size_t>(2 * pairs) * 128 * kDv * sizeof(float); }
 size_t ml_part_bytes(int pairs) { return static_cast<size_t>(2 * pairs) * 128 * sizeof(float2); }
 size_t workspace_bytes(int pairs) { return o_part_bytes(pairs) + ml_part_bytes(pairs) + pairs * sizeof(int4); }
 
+// bf16: q and the cache rows as 9 blocks of 64 dims, block-major boxes; fp8:
+// the cache's maps cover the rope dims only (128 bytes from byte 528 of a row).
+template <bool F8>
 dsa_status_t launch_dense(const DenseParams& p, const void* q, const void* kv, int pairs, cudaStream_t s) {
   CUtensorMap qmap, kvmap, ropemap, rowmap;
   const uint64_t rows = static_cast<uint64_t>(p.total_rows);
-  // rows of 9 blocks of 64 dims, as a block-major box
-  const uint64_t strides[2] = {kDk * 2, 128};
-  const uint64_t qdims[3] = {64, static_cast<uint64_t>(p.T) * p.H, 9}, kvdims[3] = {64, rows, 9};
-  const uint32_t qbox[3] = {64, 64, 9}, kvbox[3] = {64, 64, 2}, ropebox[3] = {64, 64, 1}, rowbox[2] = {64, 1};
-  const uint64_t rowdims[2] = {kDk, rows};
+  const void* base = F8 ? static_cast<const uint8_t*>(kv) + kDv + 16 : kv;
+  const uint64_t blocks = F8 ? 1 : 9, row_bytes = F8 ? kF8Row : kDk * 2;
+  const uint64_t qstrides[2] = {kDk * 2, 128}, strides[2] = {row_bytes, 128};
+  const uint64_t qdims[3] = {64, static_cast<uint64_t>(p.T) * p.H, 9}, kvdims[3] = {64, rows, blocks};
+  const uint32_t qbox[3] = {64, 64, 9}, kvbox[3] = {64, 64, F8 ? 1u : 2u}, ropebox[3] = {64, 64, 1}, rowbox[2] = {64, 1};
+  const uint64_t rowdims[2] = {64 * blocks, rows};
   const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   dsa_status_t st;
-  if ((st = make_tmap(&qmap, bf16, 3, q, qdims, strides, qbox, sw)) != DSA_OK) return st;
-  if ((st = make_tmap(&kvmap, bf16, 3, kv, kvdims, strides, kvbox, sw)) != DSA_OK) return st;
-  if ((st = make_tmap(&ropemap, bf16, 3, kv, kvdims, strides, ropebox, sw)) != DSA_OK) return st;
-  if ((st = make_tmap(&rowmap, bf16, 2, kv, rowdims, strides, rowbox, sw)) != DSA_OK) return st;
-  if ((st = allow_smem(dense_mla_kernel, kSmTotal, g_smem_dense)) != DSA_OK) return st;
+  if ((st = make_tmap(&qmap, bf16, 3, q, qdims, qstrides, qbox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&kvmap, bf16, 3, base, kvdims, strides, kvbox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&ropemap, bf16, 3, base, kvdims, strides, ropebox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&rowmap, bf16, 2, base, rowdims, strides, rowbox, sw)) != DSA_OK) return st;
+  if ((st = allow_smem(dense_mla_kernel<F8>, kSmTotal, g_smem_dense[F8])) != DSA_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreadsOf<F8>);
   cfg.dynamicSmemBytes = kSmTotal;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -810,7 +928,7 @@ dsa_status_t launch_dense(const DenseParams& p, const void* q, const void* kv, i
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_kernel, p, qmap, kvmap, ropemap, rowmap);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_kernel<F8>, p, qmap, kvmap, ropemap, rowmap);
   if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_kernel launch failed: %s", cudaGetErrorString(e));
   if (p.cut) {
     if ((st = allow_smem(dense_mla_merge_kernel, 0, g_smem_dense_merge)) != DSA_OK) return st;
@@ -822,103 +940,6 @@ dsa_status_t launch_dense(const DenseParams& p, const void* q, const void* kv, i
     if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_merge_kernel launch failed: %s", cudaGetErrorString(e));
   }
   return check_launch("dense_mla_kernel");
-}
-
-// ---------------------------------------------------------------------------
-// fp8 cache, the simple form: one warp per (token, head), the 8 warps of a CTA
-// taking 8 heads of a token; a lane holds dims {2 lane + 64 i, 2 lane + 64 i +
-// 1} of q and of the output, and the softmax runs over the keys one at a time.
-struct SimpleParams {
-  const uint16_t* q;
-  const uint8_t* kv;
-  int64_t block_bytes;
-  int32_t num_blocks;
-  const int32_t* block_table;
-  int32_t bt_stride;
-  const int32_t *seq_lens, *qsl;
-  int32_t B, T, H, block_size;
-  float scale_log2;
-  uint16_t* out;
-  float* lse;
-  int32_t* dev_status;
-};
-
-template <bool F8>
-__global__ void __launch_bounds__(256) dense_mla_simple_kernel(const __grid_constant__ SimpleParams p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x, h = blockIdx.y * 8 + warp;
-  if (h >= p.H || t >= __ldg(p.qsl + p.B)) return;
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.qsl + mid) <= t) lo = mid; else hi = mid - 1;
-  }
-  const int q0 = __ldg(p.qsl + lo), q1 = __ldg(p.qsl + lo + 1);
-  int64_t valid = static_cast<int64_t>(__ldg(p.seq_lens + lo)) - (q1 - q0) + (t - q0) + 1;
-  const int64_t cap = static_cast<int64_t>(p.bt_stride) * p.block_size;
-  if (valid < 1 || valid > cap) {
-    if (lane == 0) report(p.dev_status, DSA_DEVERR_SEQ_LEN);
-    valid = max(int64_t(0), min(valid, cap));
-  }
-  const int64_t row = static_cast<int64_t>(t) * p.H + h;
-  float2 q[9], acc[8];
-  for (int i = 0; i < 9; ++i)
-    q[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p.q + row * kDk + 64 * i + 2 * lane));
-  for (int i = 0; i < 8; ++i) acc[i] = make_float2(0.f, 0.f);
-  float m = kNegSentinel, l = 0.f;
-  const int32_t* bt = p.block_table + static_cast<int64_t>(lo) * p.bt_stride;
-  for (int64_t key = 0; key < valid; ++key) {
-    const int j = static_cast<int>(key / p.block_size);
-    const int blk = __ldg(bt + j);
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (lane == 0) report(p.dev_status, DSA_DEVERR_BLOCK_OOB);
-      key = static_cast<int64_t>(j + 1) * p.block_size - 1;
-      continue;
-    }
-    const int64_t off = key - static_cast<int64_t>(j) * p.block_size;
-    const uint8_t* src = p.kv + blk * p.block_bytes + off * (F8 ? kF8Row : 2 * kDk);
-    float2 k[9];
-    if constexpr (F8) {
-      const float4 sc = __ldg(reinterpret_cast<const float4*>(src + kDv));
-      const float s4[4] = {sc.x, sc.y, sc.z, sc.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t two;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(__ldg(reinterpret_cast<const uint16_t*>(src + 64 * i) + lane)));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
-        k[i] = make_float2(f.x * s4[i >> 1], f.y * s4[i >> 1]);
-      }
-      const uint32_t r = __ldg(reinterpret_cast<const uint32_t*>(src + kDv + 16) + lane);
-      k[8] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 9; ++i) {
-        const uint32_t r = __ldg(reinterpret_cast<const uint32_t*>(src) + 32 * i + lane);
-        k[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r));
-      }
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 9; ++i) s = fmaf(q[i].x, k[i].x, fmaf(q[i].y, k[i].y, s));
-#pragma unroll
-    for (int off2 = 16; off2 > 0; off2 >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off2);
-    s *= p.scale_log2;
-    const float m_new = fmaxf(m, s);
-    const float a = exp2f(m - m_new), w = exp2f(s - m_new);
-    l = l * a + w;
-    m = m_new;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      acc[i].x = fmaf(w, k[i].x, acc[i].x * a);
-      acc[i].y = fmaf(w, k[i].y, acc[i].y * a);
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<__nv_bfloat162*>(p.out + row * kDv + 64 * i + 2 * lane) =
-        __floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_stride, int32_t num_blocks,
@@ -960,55 +981,34 @@ dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_st
   if (need && (workspace == nullptr || ws_bytes < need || !aligned16(workspace)))
     return fail(DSA_ERR_WORKSPACE, "%s: needs %zu workspace bytes (16-byte aligned), got %zu", name, need, ws_bytes);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!f8) {
-    const int pairs = num_pairs();
-    DenseParams d = {};
-    d.num_blocks = num_blocks;
-    d.rows_per_block = static_cast<int32_t>(kv_block_stride / row);
-    d.total_rows = static_cast<int32_t>(std::max<int64_t>(num_blocks * (kv_block_stride / row), 1));
-    d.block_table = block_table;
-    d.bt_stride = bt_stride;
-    d.seq_lens = seq_lens;
-    d.qsl = query_start_loc;
-    d.B = B;
-    d.T = T;
-    d.H = H;
-    d.tpt = 128 / H;
-    d.block_size = block_size;
-    d.bs64 = block_size / 64;
-    d.scale_log2 = softmax_scale * kLog2e;
-    d.cut = num_kv_splits == 0;
-    d.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-    d.out = static_cast<uint16_t*>(out);
-    d.lse = lse;
-    if (d.cut) {
-      d.o_part = static_cast<float4*>(workspace);
-      d.ml_part = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + o_part_bytes(pairs));
-      d.desc = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(d.ml_part) + ml_part_bytes(pairs));
-    }
-    d.dev_status = dev_status;
-    return launch_dense(d, q, kv_cache, pairs, s);
+  const int pairs = num_pairs();
+  DenseParams d = {};
+  d.num_blocks = num_blocks;
+  d.rows_per_block = static_cast<int32_t>(kv_block_stride / row);
+  d.total_rows = static_cast<int32_t>(std::max<int64_t>(num_blocks * (kv_block_stride / row), 1));
+  d.block_table = block_table;
+  d.bt_stride = bt_stride;
+  d.seq_lens = seq_lens;
+  d.qsl = query_start_loc;
+  d.B = B;
+  d.T = T;
+  d.H = H;
+  d.tpt = 128 / H;
+  d.block_size = block_size;
+  d.bs64 = block_size / 64;
+  d.scale_log2 = softmax_scale * kLog2e;
+  d.kv = static_cast<const uint8_t*>(kv_cache);
+  d.cut = num_kv_splits == 0;
+  d.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+  d.out = static_cast<uint16_t*>(out);
+  d.lse = lse;
+  if (d.cut) {
+    d.o_part = static_cast<float4*>(workspace);
+    d.ml_part = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + o_part_bytes(pairs));
+    d.desc = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(d.ml_part) + ml_part_bytes(pairs));
   }
-  SimpleParams p;
-  p.q = static_cast<const uint16_t*>(q);
-  p.kv = static_cast<const uint8_t*>(kv_cache);
-  p.block_bytes = f8 ? kv_block_stride : 2 * kv_block_stride;
-  p.num_blocks = num_blocks;
-  p.block_table = block_table;
-  p.bt_stride = bt_stride;
-  p.seq_lens = seq_lens;
-  p.qsl = query_start_loc;
-  p.B = B;
-  p.T = T;
-  p.H = H;
-  p.block_size = block_size;
-  p.scale_log2 = softmax_scale * kLog2e;
-  p.out = static_cast<uint16_t*>(out);
-  p.lse = lse;
-  p.dev_status = dev_status;
-  const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>((H + 7) / 8));
-  dense_mla_simple_kernel<true><<<grid, 256, 0, s>>>(p);
-  return check_launch("dense_mla_simple_kernel");
+  d.dev_status = dev_status;
+  return f8 ? launch_dense<true>(d, q, kv_cache, pairs, s) : launch_dense<false>(d, q, kv_cache, pairs, s);
 }
 
 }  // namespace
