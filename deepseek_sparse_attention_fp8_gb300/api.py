@@ -395,12 +395,22 @@ def dsa_mla_kv_fp8_quant_and_cache(kv, kv_cache, block_table, seq_lens, query_st
     return kv_cache
 
 
-def _same_device(**tensors):
-    """Every tensor given lies on the current CUDA device, whose stream and kernels the call uses."""
-    cur = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+def _arg(t, dtype, dims, name, dev):
+    """The address of a tensor argument: contiguous, of this dtype and rank, on
+    the current device `dev`, whose stream and kernels the call uses."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+            and t.dim() == dims):
+        return t.data_ptr()
+    _need(t, dtype, name, dims)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _status_arg(dev_status, dev):
+    return None if dev_status is None else _arg(dev_status, torch.int32, dev_status.dim(), "dev_status", dev)
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, free_blocks=None, free_head=None,
@@ -411,65 +421,65 @@ def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, fre
     [max_tokens]) and grows block_table [B, bt_stride] in place by blocks of
     the queue free_blocks, from *free_head on; free_head_out (default: in
     place) receives the advanced head."""
-    _need(ctx_lens, torch.int32, "ctx_lens", 1)
-    _need(new_lens, torch.int32, "new_lens", 1)
-    _need(block_table, torch.int32, "block_table", 2)
-    B, dev = ctx_lens.shape[0], ctx_lens.device
+    i32, dev = torch.int32, torch.cuda.current_device()
+    ctx_p, new_p = _arg(ctx_lens, i32, 1, "ctx_lens", dev), _arg(new_lens, i32, 1, "new_lens", dev)
+    table_p = _arg(block_table, i32, 2, "block_table", dev)
+    B = ctx_lens.shape[0]
     if new_lens.shape[0] != B or block_table.shape[0] < B:
         raise ValueError("new_lens and block_table must have a row per request of ctx_lens")
+    free_p = head_p = head_out_p = None
     if free_blocks is not None:
-        _need(free_blocks, torch.int32, "free_blocks", 1)
         free_head_out = free_head if free_head_out is None else free_head_out
-        _need(free_head, torch.int32, "free_head", 1)
-        _need(free_head_out, torch.int32, "free_head_out", 1)
-        if free_head.numel() < 1 or free_head_out.numel() < 1:
+        free_p = _arg(free_blocks, i32, 1, "free_blocks", dev)
+        head_p, head_out_p = _arg(free_head, i32, 1, "free_head", dev), _arg(free_head_out, i32, 1, "free_head_out", dev)
+        if not head_p or not head_out_p:
             raise ValueError("free_head and free_head_out must have an element")
-    outs = {}
-    for name, t, n, dt in (("seq_lens", seq_lens, B, torch.int32),
-                           ("query_start_loc", query_start_loc, B + 1, torch.int32),
-                           ("token_req", token_req, max_tokens, torch.int32),
-                           ("positions", positions, max_tokens, torch.int32),
-                           ("slot_map", slot_map, max_tokens, torch.int64)):
-        if t is None:
-            t = torch.empty(max(n, 0), dtype=dt, device=dev)
-        _need(t, dt, name, 1)
-        if t.shape[0] < n:
-            raise ValueError(f"{name} needs {n} elements, has {t.shape[0]}")
-        outs[name] = t
-    if dev_status is not None:
-        _need(dev_status, torch.int32, "dev_status")
-    _same_device(ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table, free_blocks=free_blocks,
-                 free_head=free_head, free_head_out=free_head_out, dev_status=dev_status, **outs)
-    # an empty queue has no address of its own, and NULL would mean "take no blocks"
-    queue = free_blocks if free_blocks is None or free_blocks.numel() else free_head
-    st = lib.dsa_build_batch(_ptr(ctx_lens), _ptr(new_lens), B, block_size, _ptr(queue),
-                             0 if free_blocks is None else free_blocks.shape[0], _ptr(free_head), _ptr(free_head_out),
-                             _ptr(block_table), block_table.shape[1], max_tokens, _ptr(outs["seq_lens"]),
-                             _ptr(outs["query_start_loc"]), _ptr(outs["token_req"]), _ptr(outs["positions"]),
-                             _ptr(outs["slot_map"]), _ptr(dev_status), _stream(stream))
+        free_p = free_p or head_p  # an empty queue has no address of its own, and NULL would mean "take no blocks"
+    n = max(max_tokens, 0)
+    if seq_lens is None:
+        seq_lens = torch.empty(B, dtype=i32, device=ctx_lens.device)
+    if query_start_loc is None:
+        query_start_loc = torch.empty(B + 1, dtype=i32, device=ctx_lens.device)
+    if token_req is None:
+        token_req = torch.empty(n, dtype=i32, device=ctx_lens.device)
+    if positions is None:
+        positions = torch.empty(n, dtype=i32, device=ctx_lens.device)
+    if slot_map is None:
+        slot_map = torch.empty(n, dtype=torch.int64, device=ctx_lens.device)
+    outs = (seq_lens, query_start_loc, token_req, positions, slot_map)
+    seq_p, qsl_p = _arg(seq_lens, i32, 1, "seq_lens", dev), _arg(query_start_loc, i32, 1, "query_start_loc", dev)
+    req_p, pos_p = _arg(token_req, i32, 1, "token_req", dev), _arg(positions, i32, 1, "positions", dev)
+    slot_p = _arg(slot_map, torch.int64, 1, "slot_map", dev)
+    for t, need, name in zip(outs, (B, B + 1, n, n, n), ("seq_lens", "query_start_loc", "token_req", "positions",
+                                                         "slot_map")):
+        if t.shape[0] < need:
+            raise ValueError(f"{name} needs {need} elements, has {t.shape[0]}")
+    st = lib.dsa_build_batch(ctx_p, new_p, B, block_size, free_p, 0 if free_blocks is None else free_blocks.shape[0],
+                             head_p, head_out_p, table_p, block_table.shape[1], max_tokens, seq_p, qsl_p, req_p, pos_p,
+                             slot_p, _status_arg(dev_status, dev), _raw_stream(stream))
     _check(st, "dsa_build_batch")
-    return tuple(outs.values())
+    return outs
 
 
 def dsa_mla_kv_cache(kv, slot_map, kv_cache, dev_status=None, stream=None):
     """Stores the latent rows kv [T, Dk] (bf16; rows may be strided) at their
     slots (int64 [T], -1 = skip) of the bf16 latent cache kv_cache
     [num_blocks, block_size, Dk] in place."""
+    dev = torch.cuda.current_device()
     if not isinstance(kv, torch.Tensor) or kv.dtype != torch.bfloat16 or kv.dim() != 2 or not kv.is_cuda:
         raise TypeError("kv must be a two-dimensional bfloat16 CUDA tensor")
+    if kv.get_device() != dev:
+        raise ValueError(f"kv is on {kv.device}, the current device is cuda:{dev}")
     T, Dk = kv.shape
     if Dk > 1 and kv.stride(1) != 1:
         raise ValueError("the values of a row of kv must be contiguous")
-    _need(slot_map, torch.int64, "slot_map", 1)
-    _need(kv_cache, torch.bfloat16, "kv_cache", 3)
-    if slot_map.shape[0] < T or kv_cache.shape[2] != Dk:
+    slot_p = _arg(slot_map, torch.int64, 1, "slot_map", dev)
+    cache_p = _arg(kv_cache, torch.bfloat16, 3, "kv_cache", dev)
+    nb, bs, row = kv_cache.shape
+    if slot_map.shape[0] < T or row != Dk:
         raise ValueError("slot_map needs an entry per row of kv, and kv_cache rows as wide as kv's")
-    if dev_status is not None:
-        _need(dev_status, torch.int32, "dev_status")
-    _same_device(kv=kv, slot_map=slot_map, kv_cache=kv_cache, dev_status=dev_status)
-    nb, bs, _ = kv_cache.shape
-    st = lib.dsa_mla_kv_cache(_ptr(kv), kv.stride(0) if T > 1 else Dk, T, Dk, _ptr(slot_map), _ptr(kv_cache), bs * Dk,
-                              nb, bs, _ptr(dev_status), _stream(stream))
+    st = lib.dsa_mla_kv_cache(kv.data_ptr(), kv.stride(0) if T > 1 else Dk, T, Dk, slot_p, cache_p, bs * Dk, nb, bs,
+                              _status_arg(dev_status, dev), _raw_stream(stream))
     _check(st, "dsa_mla_kv_cache")
     return kv_cache
 
@@ -478,39 +488,39 @@ def dense_mla_workspace_size(T: int, H: int, Dv: int, num_kv_splits: int) -> int
     return int(lib.dense_mla_workspace_size(T, H, Dv, num_kv_splits))
 
 
-def _dense_mla(name, q, kv_cache, cache_dtype, block_table, seq_lens, query_start_loc, softmax_scale, dv, out, lse,
-               num_kv_splits, workspace, dev_status, stream):
-    _need(q, torch.bfloat16, "q", 3)
-    _need(kv_cache, cache_dtype, "kv_cache", 3)
-    _need(block_table, torch.int32, "block_table", 2)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
-    _need(query_start_loc, torch.int32, "query_start_loc", 1)
-    _need(out, torch.bfloat16, "out", 3)
+def _dense_mla(name, call, q, kv_cache, cache_dtype, block_table, seq_lens, query_start_loc, softmax_scale, dv, out,
+               lse, num_kv_splits, workspace, dev_status, stream):
+    i32, bf16, dev = torch.int32, torch.bfloat16, torch.cuda.current_device()
+    q_p, cache_p = _arg(q, bf16, 3, "q", dev), _arg(kv_cache, cache_dtype, 3, "kv_cache", dev)
+    table_p, seq_p = _arg(block_table, i32, 2, "block_table", dev), _arg(seq_lens, i32, 1, "seq_lens", dev)
+    qsl_p, out_p = _arg(query_start_loc, i32, 1, "query_start_loc", dev), _arg(out, bf16, 3, "out", dev)
     T, H, Dk = q.shape
     B = seq_lens.shape[0]
     num_blocks, block_size, row = kv_cache.shape
-    if tuple(out.shape) != (T, H, dv):
+    if out.shape != (T, H, dv):
         raise ValueError(f"out must be {(T, H, dv)}, got {tuple(out.shape)}")
-    if row != (Dk if cache_dtype == torch.bfloat16 else MLA_FP8_ROW_BYTES):
+    if row != (Dk if cache_dtype is bf16 else MLA_FP8_ROW_BYTES):
         raise ValueError(f"kv_cache rows of {row} elements do not fit q's {Dk} dims")
     if block_table.shape[0] < B or query_start_loc.shape[0] != B + 1:
         raise ValueError("block_table needs a row per request, query_start_loc one entry more than seq_lens")
+    lse_p = None
     if lse is not None:
-        _need(lse, torch.float32, "lse", 2)
-        if tuple(lse.shape) != (T, H):
+        lse_p = _arg(lse, torch.float32, 2, "lse", dev)
+        if lse.shape != (T, H):
             raise ValueError(f"lse must be {(T, H)}, got {tuple(lse.shape)}")
-    if dev_status is not None:
-        _need(dev_status, torch.int32, "dev_status")
-    need = dense_mla_workspace_size(T, H, dv, num_kv_splits)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _same_device(q=q, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, query_start_loc=query_start_loc,
-                 out=out, lse=lse, workspace=workspace, dev_status=dev_status)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = getattr(lib, name)(_ptr(q), _ptr(kv_cache), block_size * row, num_blocks, _ptr(block_table),
-                            block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc), B, T, H, Dk, dv, block_size,
-                            softmax_scale, num_kv_splits, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
-                            _ptr(dev_status), _stream(stream))
+    ws_p, ws_bytes = None, 0
+    if num_kv_splits == 0:
+        need = lib.dense_mla_workspace_size(T, H, dv, 0)
+        if workspace is not None:
+            ws_bytes = workspace.numel() * workspace.element_size()
+        if ws_bytes < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws_bytes = need
+        if workspace is not None:
+            ws_p = _arg(workspace, workspace.dtype, workspace.dim(), "workspace", dev)
+    st = call(q_p, cache_p, block_size * row, num_blocks, table_p, block_table.shape[1], seq_p, qsl_p, B, T, H, Dk, dv,
+              block_size, softmax_scale, num_kv_splits, out_p, lse_p, ws_p, ws_bytes, _status_arg(dev_status, dev),
+              _raw_stream(stream))
     _check(st, name)
     return out
 
@@ -521,12 +531,14 @@ def dense_mla_attention(q, kv_cache, block_table, seq_lens, query_start_loc, sof
     cache [blocks, block_size, Dk]: out [T,H,Dv] (bf16), lse [T,H].
     num_kv_splits: 0 spreads the keys over the GPU, -1 or 1 never cuts a
     token's keys (results independent of the batch)."""
-    return _dense_mla("dense_mla_attention", q, kv_cache, torch.bfloat16, block_table, seq_lens, query_start_loc,
-                      softmax_scale, dv, out, lse, num_kv_splits, workspace, dev_status, stream)
+    return _dense_mla("dense_mla_attention", lib.dense_mla_attention, q, kv_cache, torch.bfloat16, block_table,
+                      seq_lens, query_start_loc, softmax_scale, dv, out, lse, num_kv_splits, workspace, dev_status,
+                      stream)
 
 
 def dense_mla_attention_fp8(q, kv_cache, block_table, seq_lens, query_start_loc, softmax_scale, dv, out, lse=None,
                             num_kv_splits=0, workspace=None, dev_status=None, stream=None):
     """dense_mla_attention over the fp8 latent cache [blocks, block_size, 656] (uint8)."""
-    return _dense_mla("dense_mla_attention_fp8", q, kv_cache, torch.uint8, block_table, seq_lens, query_start_loc,
-                      softmax_scale, dv, out, lse, num_kv_splits, workspace, dev_status, stream)
+    return _dense_mla("dense_mla_attention_fp8", lib.dense_mla_attention_fp8, q, kv_cache, torch.uint8, block_table,
+                      seq_lens, query_start_loc, softmax_scale, dv, out, lse, num_kv_splits, workspace, dev_status,
+                      stream)

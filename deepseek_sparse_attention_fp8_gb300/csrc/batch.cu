@@ -3,11 +3,14 @@
 // of free blocks (another prefix sum, of ceil((ctx+new)/bs) - ceil(ctx/bs)),
 // and per token its request, position and cache slot.
 //
-// The requests are taken in chunks of one per thread: a chunk's two prefix
-// sums are block scans with a carry, then the threads share the chunk's
-// tokens, each finding its request by binary search in shared memory. A
-// token at the first position of a new block stores the block in the table,
-// so no thread walks a long request's blocks alone.
+// One cluster of CTAs (of one CTA for a small batch), so that the queue's head
+// can be read by all and advanced in place behind a cluster barrier. The
+// requests are taken in chunks of one per thread: every CTA makes a chunk's
+// two prefix sums (block scans with a carry) itself, then the cluster's
+// threads share the chunk's tokens, four in a row each: one binary search in
+// shared memory, and full 16-byte stores. A token at the first position of a
+// new block stores the block in the table, so no thread walks a long
+// request's blocks alone.
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -15,6 +18,7 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 1024;
+constexpr int kCluster = 8, kOneCta = 4096;
 
 struct BatchParams {
   const int32_t *ctx, *add, *free_blocks, *free_head;
@@ -23,6 +27,7 @@ struct BatchParams {
   int32_t B, block_size, num_free, bt_stride, max_tokens;
   int32_t *seq_lens, *qsl, *token_req, *positions;
   int64_t* slot_map;
+  int32_t vec;  // token_req, positions and slot_map are 16-byte aligned
   int32_t* dev_status;
 };
 
@@ -50,7 +55,8 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
 __global__ void __launch_bounds__(kThreads) build_batch_kernel(const __grid_constant__ BatchParams p) {
   __shared__ int64_t warp_sums[kThreads / 32];
   __shared__ int32_t s_start[kThreads + 1], s_ctx[kThreads], s_take[kThreads];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, rank = blockIdx.x;  // the grid is one cluster
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
   uint32_t err = 0;
   const int64_t head = p.free_blocks != nullptr ? *p.free_head : 0;
   const bool head_ok = head >= 0 && head <= p.num_free;
@@ -86,55 +92,87 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const __grid_cons
       // end all are alike (none left)
       s_take[tid] = static_cast<int32_t>(min(head + take_end - take, int64_t(INT32_MAX)));
       if (tid == n - 1) s_start[n] = static_cast<int32_t>(start + a);
-      p.seq_lens[b] = static_cast<int32_t>(c + a);
-      p.qsl[b] = static_cast<int32_t>(start);
-      if (b == p.B - 1) p.qsl[p.B] = static_cast<int32_t>(start + a);
+      if (rank == 0) {
+        p.seq_lens[b] = static_cast<int32_t>(c + a);
+        p.qsl[b] = static_cast<int32_t>(start);
+        if (b == p.B - 1) p.qsl[p.B] = static_cast<int32_t>(start + a);
+      }
     }
     tokens += sum;
     taken += sum_take;
     __syncthreads();
-    for (int t = s_start[0] + tid; t < s_start[n]; t += kThreads) {
-      int lo = 0, hi = n - 1;  // the last request that starts at or before t
+    const int first = s_start[0], end = s_start[n];
+    // four tokens from a multiple of 4 on; the chunk may begin and end inside
+    for (int64_t t0 = (first & ~3) + 4 * (rank * kThreads + tid); t0 < end; t0 += 4 * step) {
+      const int ta = max(static_cast<int>(t0), first);
+      int lo = 0, hi = n - 1;  // the last request that starts at or before the first token
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (s_start[mid] <= t) lo = mid; else hi = mid - 1;
+        if (s_start[mid] <= ta) lo = mid; else hi = mid - 1;
       }
-      const int req = b0 + lo;
-      const int32_t pos = s_ctx[lo] + (t - s_start[lo]);
-      const int j = pos / p.block_size, off = pos - j * p.block_size;
-      const int held_r = (s_ctx[lo] - 1) / p.block_size + (s_ctx[lo] > 0 ? 1 : 0);
-      int64_t slot = -1;
-      if (j >= p.bt_stride) {
-        err |= DSA_DEVERR_SEQ_LEN;
-      } else {
-        int32_t* entry = p.table + static_cast<int64_t>(req) * p.bt_stride + j;
-        int32_t blk;
-        if (j >= held_r && p.free_blocks != nullptr) {
-          const int64_t at = static_cast<int64_t>(s_take[lo]) + (j - held_r);
-          const bool got = head_ok && at < p.num_free;
-          blk = got ? __ldg(p.free_blocks + at) : -1;
-          if (!got) err |= DSA_DEVERR_NO_BLOCKS;
-          else if (blk < 0) err |= DSA_DEVERR_BLOCK_OOB;
-          if (off == 0) *entry = blk;
-        } else {
-          blk = *entry;
-          if (blk < 0) err |= DSA_DEVERR_BLOCK_OOB;
+      int32_t req[4], pos[4];
+      int64_t slot[4];
+      int last_req = -1, last_j = -1;
+      int32_t blk = -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t t = t0 + i;
+        req[i] = pos[i] = 0;
+        slot[i] = 0;
+        if (t < first || t >= end) continue;
+        while (t >= s_start[lo + 1]) ++lo;  // ends before n: t < s_start[n]
+        pos[i] = s_ctx[lo] + (static_cast<int>(t) - s_start[lo]);
+        req[i] = b0 + lo;
+        const int j = pos[i] / p.block_size, off = pos[i] - j * p.block_size;
+        slot[i] = -1;
+        if (j >= p.bt_stride) {
+          err |= DSA_DEVERR_SEQ_LEN;
+          continue;
         }
-        if (blk >= 0) slot = static_cast<int64_t>(blk) * p.block_size + off;
+        if (lo != last_req || j != last_j) {
+          last_req = lo;
+          last_j = j;
+          int32_t* entry = p.table + static_cast<int64_t>(b0 + lo) * p.bt_stride + j;
+          const int held = (s_ctx[lo] - 1) / p.block_size + (s_ctx[lo] > 0 ? 1 : 0);
+          if (j >= held && p.free_blocks != nullptr) {
+            const int64_t at = static_cast<int64_t>(s_take[lo]) + (j - held);
+            const bool got = head_ok && at < p.num_free;
+            blk = got ? __ldg(p.free_blocks + at) : -1;
+            if (!got) err |= DSA_DEVERR_NO_BLOCKS;
+            else if (blk < 0) err |= DSA_DEVERR_BLOCK_OOB;
+            if (off == 0) *entry = blk;
+          } else {
+            blk = *entry;
+            if (blk < 0) err |= DSA_DEVERR_BLOCK_OOB;
+          }
+        }
+        if (blk >= 0) slot[i] = static_cast<int64_t>(blk) * p.block_size + off;
       }
-      p.token_req[t] = req;
-      p.positions[t] = pos;
-      p.slot_map[t] = slot;
+      if (p.vec && t0 >= first && t0 + 4 <= end) {
+        *reinterpret_cast<int4*>(p.token_req + t0) = make_int4(req[0], req[1], req[2], req[3]);
+        *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        reinterpret_cast<longlong2*>(p.slot_map + t0)[0] = make_longlong2(slot[0], slot[1]);
+        reinterpret_cast<longlong2*>(p.slot_map + t0)[1] = make_longlong2(slot[2], slot[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (t0 + i < first || t0 + i >= end) continue;
+          p.token_req[t0 + i] = req[i];
+          p.positions[t0 + i] = pos[i];
+          p.slot_map[t0 + i] = slot[i];
+        }
+      }
     }
     __syncthreads();
   }
-  if (p.B == 0 && tid == 0) p.qsl[0] = 0;
-  for (int64_t t = min(tokens, int64_t(p.max_tokens)) + tid; t < p.max_tokens; t += kThreads) {
+  if (p.B == 0 && rank == 0 && tid == 0) p.qsl[0] = 0;
+  for (int64_t t = min(tokens, int64_t(p.max_tokens)) + rank * kThreads + tid; t < p.max_tokens; t += step) {
     p.token_req[t] = -1;
     p.positions[t] = 0;
     p.slot_map[t] = -1;
   }
-  if (tid == 0 && p.free_blocks != nullptr)
+  if (gridDim.x > 1) ptx::cluster_sync_all();  // every CTA has read the head
+  if (rank == 0 && tid == 0 && p.free_blocks != nullptr)
     *p.free_head_out = static_cast<int32_t>(head_ok ? min(head + taken, int64_t(p.num_free)) : head);
   if (err) report(p.dev_status, err);
 }
@@ -161,6 +199,8 @@ extern "C" dsa_status_t dsa_build_batch(const int32_t* ctx_lens, const int32_t* 
     return fail(DSA_ERR_INVALID_ARG, "dsa_build_batch: free_blocks without free_head and free_head_out");
   if (!free_blocks && num_free > 0)
     return fail(DSA_ERR_INVALID_ARG, "dsa_build_batch: num_free without free_blocks");
+  if (B > 0 && (seq_lens == ctx_lens || seq_lens == new_lens || query_start_loc == ctx_lens || query_start_loc == new_lens))
+    return fail(DSA_ERR_INVALID_ARG, "dsa_build_batch: seq_lens and query_start_loc must not share the inputs' memory");
   dsa_status_t st = check_device();
   if (st != DSA_OK) return st;
   BatchParams p;
@@ -181,6 +221,21 @@ extern "C" dsa_status_t dsa_build_batch(const int32_t* ctx_lens, const int32_t* 
   p.positions = positions;
   p.slot_map = slot_map;
   p.dev_status = dev_status;
-  build_batch_kernel<<<1, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  p.vec = aligned16(token_req) && aligned16(positions) && aligned16(slot_map);
+  // a CTA serves up to kOneCta tokens about as fast as a cluster does, whose
+  // launch and barrier cost more
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(max_tokens <= kOneCta ? 1 : kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cfg.gridDim.x;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, build_batch_kernel, p);
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "build_batch_kernel launch failed: %s", cudaGetErrorString(e));
   return check_launch("build_batch_kernel");
 }

@@ -343,6 +343,7 @@ dsa_status_t dsa_mla_kv_fp8_quant_and_cache(const void* kv, int64_t kv_stride_t,
  *              query_start_loc[b] and its cache slot block * block_size +
  *              position % block_size. Rows from the batch's token count up to
  *              max_tokens (a padded buffer) get -1, 0 and -1.
+ * seq_lens and query_start_loc must not share memory with the lengths given.
  * What only the device sees: a negative length, or one whose ctx + new passes
  * 2^31 - 1, counts as 0 new tokens (and a negative ctx as 0); new tokens past
  * max_tokens are dropped from the batch, the last requests' first; both set

@@ -51,6 +51,9 @@ def test_build_batch_rejects_bad_arguments(api):
                dict(head=NULL), dict(head_out=NULL), dict(free=NULL)):
         assert call(**kw) == api.DSA_ERR_INVALID_ARG, kw
     assert call(bs=32) == api.DSA_ERR_UNSUPPORTED
+    other = ctypes.c_void_p(1 << 21)
+    assert call(seq=other, qsl=FAKE) == api.DSA_ERR_INVALID_ARG  # outputs in the inputs' memory
+    assert call(seq=FAKE, qsl=other) == api.DSA_ERR_INVALID_ARG
 
 
 def test_kv_cache_rejects_bad_arguments(api):
