@@ -409,8 +409,9 @@ def _status_arg(dev_status, dev):
     return None if dev_status is None else _arg(dev_status, torch.int32, dev_status.dim(), "dev_status", dev)
 
 
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _raw_stream(stream, dev):
+    # without a stream object, whose making costs as much as a launch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, free_blocks=None, free_head=None,
@@ -456,7 +457,7 @@ def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, fre
             raise ValueError(f"{name} needs {need} elements, has {t.shape[0]}")
     st = lib.dsa_build_batch(ctx_p, new_p, B, block_size, free_p, 0 if free_blocks is None else free_blocks.shape[0],
                              head_p, head_out_p, table_p, block_table.shape[1], max_tokens, seq_p, qsl_p, req_p, pos_p,
-                             slot_p, _status_arg(dev_status, dev), _raw_stream(stream))
+                             slot_p, _status_arg(dev_status, dev), _raw_stream(stream, dev))
     _check(st, "dsa_build_batch")
     return outs
 
@@ -479,7 +480,7 @@ def dsa_mla_kv_cache(kv, slot_map, kv_cache, dev_status=None, stream=None):
     if slot_map.shape[0] < T or row != Dk:
         raise ValueError("slot_map needs an entry per row of kv, and kv_cache rows as wide as kv's")
     st = lib.dsa_mla_kv_cache(kv.data_ptr(), kv.stride(0) if T > 1 else Dk, T, Dk, slot_p, cache_p, bs * Dk, nb, bs,
-                              _status_arg(dev_status, dev), _raw_stream(stream))
+                              _status_arg(dev_status, dev), _raw_stream(stream, dev))
     _check(st, "dsa_mla_kv_cache")
     return kv_cache
 
@@ -520,7 +521,7 @@ def _dense_mla(name, call, q, kv_cache, cache_dtype, block_table, seq_lens, quer
             ws_p = _arg(workspace, workspace.dtype, workspace.dim(), "workspace", dev)
     st = call(q_p, cache_p, block_size * row, num_blocks, table_p, block_table.shape[1], seq_p, qsl_p, B, T, H, Dk, dv,
               block_size, softmax_scale, num_kv_splits, out_p, lse_p, ws_p, ws_bytes, _status_arg(dev_status, dev),
-              _raw_stream(stream))
+              _raw_stream(stream, dev))
     _check(st, name)
     return out
 

@@ -42,17 +42,18 @@ constexpr int kDk = 576, kDv = 512, kF8Row = 656;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// warps 0-7 softmax, 8 q / rope (bf16 cache: and the other keys), 9 MMA, then
-// the own keys: one warp of TMA copies, or (fp8 cache) 8 decoding warps, and 4
-// more for the other keys
-constexpr int kAuxWarp = 8, kMmaWarp = 9, kKeyWarp = 10, kKeyWarpsF8 = 8, kOtherWarpsF8 = 4;
-constexpr int kOtherWarp = kKeyWarp + kKeyWarpsF8;  // fp8 only
+// Warps 0-7 softmax, 8 q / rope (bf16 cache: and the other keys), 9 MMA, then
+// the own keys: one warp of TMA copies, or (fp8 cache) 8 decoding warps, which
+// take the other keys too. Nothing may spill: beside 227 KB of shared memory
+// the L1 is so small that spilled registers come back from L2.
+constexpr int kAuxWarp = 8, kMmaWarp = 9, kKeyWarp = 10, kDecodeWarps = 8;
 template <bool F8>
-constexpr int kThreadsOf = 32 * (F8 ? kOtherWarp + kOtherWarpsF8 : kKeyWarp + 1);
+constexpr int kThreadsOf = 32 * (kKeyWarp + (F8 ? kDecodeWarps : 1));
 constexpr int kTile = 128;
 constexpr int kSlot = 16384;  // 64 keys x 128 dims
 constexpr float kRescaleThreshold = 8.f;  // log2 units
 constexpr long long kWaitLimitCycles = 2000000000ll;
+constexpr int kAhead = 3;   // steps (fp8 cache)
 constexpr int kMinRun = 4;  // steps a run has at least when row tiles may be cut
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;  // O 256 columns, S 2 x 64
 
@@ -73,6 +74,7 @@ struct Bars {
   uint64_t pv_half[2];   // the first 64 keys of a step have entered O (in both CTAs)
   uint64_t pv_done[2];   // O += P V of a step complete (in both CTAs)
   uint64_t rows[2];      // the four softmax warps that share 32 rows
+  uint64_t first;        // q and the rope dims of the run's first step have been asked for
   uint32_t tmem;
   volatile int abort;
   // the run: first request, row tile and step of it, and the units [pos, end)
@@ -104,7 +106,7 @@ struct DenseParams {
 // last token sees / 128)).
 struct Request {
   int32_t q0, q_len, n_tiles, kv_len;  // kv_len: its cached keys that the table can hold
-  int64_t c;     // position of its first new token
+  int32_t c;     // position of its first new token (a length below 0 counts as 0)
   bool uneven;   // lengths that contradict each other: every tile is charged kv_len
 };
 
@@ -115,18 +117,19 @@ __device__ __forceinline__ Request load_request(const DenseParams& p, int b) {
   r.q0 = q0;
   r.q_len = max(q1 - q0, 0);
   r.n_tiles = (r.q_len + p.tpt - 1) / p.tpt;
+  // at most 2^31 - 256, so that sums of a few steps stay within 31 bits
   r.kv_len = static_cast<int32_t>(max(int64_t(0), min(min(sl, cap), int64_t(0x7FFFFF00))));
-  r.c = sl - r.q_len;
+  r.c = static_cast<int32_t>(max(sl, int64_t(0))) - r.q_len;
   r.uneven = r.c < 0 || r.kv_len != sl;
   return r;
 }
 // keys visible to the token i (from 0) of the request
 __device__ __forceinline__ int visible(const Request& r, int i) {
-  return static_cast<int>(max(int64_t(0), min(r.c + i + 1, int64_t(r.kv_len))));
+  return max(0, min(r.c + i + 1, r.kv_len));
 }
 __device__ __forceinline__ int steps_of(const DenseParams& p, const Request& r, int tile) {
   const int keys = r.uneven ? r.kv_len : visible(r, min(r.q_len, (tile + 1) * p.tpt) - 1);
-  return max(1, static_cast<int>((static_cast<int64_t>(keys) + kTile - 1) / kTile));
+  return max(1, (keys + kTile - 1) / kTile);
 }
 // sum over i < n of floor((a i + b) / 128)
 __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
@@ -158,34 +161,32 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
 __device__ __forceinline__ int64_t steps_before(const DenseParams& p, const Request& r, int n) {
   if (r.uneven) return static_cast<int64_t>(n) * steps_of(p, r, 0);
   if (n == 0) return 0;
-  if (n < r.n_tiles) return floor_sum(n, p.tpt, r.c + p.tpt + kTile - 1);
-  return floor_sum(n - 1, p.tpt, r.c + p.tpt + kTile - 1) + steps_of(p, r, n - 1);
+  if (n < r.n_tiles) return floor_sum(n, p.tpt, static_cast<int64_t>(r.c) + p.tpt + kTile - 1);
+  return floor_sum(n - 1, p.tpt, static_cast<int64_t>(r.c) + p.tpt + kTile - 1) + steps_of(p, r, n - 1);
 }
 
 // A run of steps, segment by segment (a segment: the steps of one row tile).
 struct Cursor {
   Request req;
   int32_t b, tile, nk, k0, k1;
-  int64_t pos, end;
+  int32_t left;  // steps of the run from this segment on
   __device__ __forceinline__ void cut(const DenseParams& p) {
     nk = steps_of(p, req, tile);
-    k1 = nk;
-    if (p.cut && end - pos < k1 - k0) k1 = k0 + static_cast<int32_t>(end - pos);
+    k1 = p.cut ? min(nk, k0 + left) : nk;
   }
   __device__ __forceinline__ bool start(const DenseParams& p, const Bars* s) {
     b = s->b;
     tile = s->tile;
-    k0 = s->k0;
-    pos = s->pos;
-    end = s->end;
-    if (pos >= end) return false;
+    k0 = k1 = nk = s->k0;
+    left = static_cast<int32_t>(s->end - s->pos);
+    if (left <= 0) return false;
     req = load_request(p, b);
     cut(p);
     return true;
   }
   __device__ __forceinline__ bool next(const DenseParams& p) {
-    pos += k1 - k0;
-    if (pos >= end) return false;
+    left -= k1 - k0;
+    if (left <= 0) return false;
     k0 = 0;
     if (++tile >= req.n_tiles) {
       tile = 0;
@@ -199,25 +200,46 @@ struct Cursor {
   }
 };
 
-// The cache rows of 64 keys from key0 on: their first row (total_rows, which
+// The cache rows of a unit of 64 keys: their first row (total_rows, which
 // reads as zeros, where there is none) and how many of them exist.
 struct Rows {
   int32_t row, n;
 };
-__device__ __forceinline__ Rows rows_of(const DenseParams& p, int b, int kv_len, int key64, bool rep) {
-  Rows x{p.total_rows, 0};
-  const int left = kv_len - key64 * 64;
-  if (left <= 0) return x;
-  const int j = key64 / p.bs64;
-  const int blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.bt_stride + j);
-  if (blk < 0 || blk >= p.num_blocks) {
-    if (rep) report(p.dev_status, DSA_DEVERR_BLOCK_OOB);
-    return x;
+// A warp's view of a row tile's part of the block table: lane l holds the
+// entry of unit base + l, and the entries of the 32 units behind are in flight,
+// so that no step waits for the table. Called by whole warps.
+struct Units {
+  int32_t base, row, ahead;
+  __device__ __forceinline__ int32_t entry(const DenseParams& p, const Cursor& c, int unit) const {
+    const int64_t key = static_cast<int64_t>(unit) * 64;
+    return key < c.req.kv_len ? __ldg(p.block_table + static_cast<int64_t>(c.b) * p.bt_stride + unit / p.bs64) : 0;
   }
-  x.row = blk * p.rows_per_block + (key64 - j * p.bs64) * 64;
-  x.n = min(left, 64);
-  return x;
-}
+  __device__ __forceinline__ int32_t first_row(const DenseParams& p, const Cursor& c, int32_t blk, int unit, bool rep) const {
+    if (blk < 0 || blk >= p.num_blocks) {
+      if (rep && static_cast<int64_t>(unit) * 64 < c.req.kv_len) report(p.dev_status, DSA_DEVERR_BLOCK_OOB);
+      return -1;
+    }
+    return blk * p.rows_per_block + (unit % p.bs64) * 64;
+  }
+  __device__ __forceinline__ void start(const DenseParams& p, const Cursor& c, int lane, bool rep) {
+    base = 2 * c.k0;
+    row = entry(p, c, base + lane);
+    ahead = entry(p, c, base + 32 + lane);
+    row = first_row(p, c, row, base + lane, rep);
+  }
+  // units are asked for in ascending order, at most 32 behind the last
+  __device__ __forceinline__ Rows get(const DenseParams& p, const Cursor& c, int unit, int lane, bool rep) {
+    if (unit >= base + 32) {
+      base += 32;
+      row = first_row(p, c, ahead, base + lane, rep);
+      ahead = entry(p, c, base + 32 + lane);
+    }
+    const int left = c.req.kv_len - unit * 64;
+    const int32_t first = __shfl_sync(0xFFFFFFFFu, row, (unit - base) & 31);
+    if (left <= 0 || first < 0) return {p.total_rows, 0};
+    return {first, min(left, 64)};
+  }
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -251,22 +273,49 @@ __device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* box, 
 // straight into registers, decoded (code * scale in fp32, rounded to bf16:
 // the tensor cores take bf16) and stored as the swizzled tile the copies of
 // the bf16 cache would bring.
+__device__ __forceinline__ float2 mul2(float2 a, float s) {  // two products in one instruction
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmul.rn.f32x2 c, a, b;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(s));
+  return r;
+}
 __device__ __forceinline__ uint32_t decode2(uint32_t two, float sc) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack_bf16(f.x * sc, f.y * sc);
+  const float2 v = mul2(f, sc);
+  return pack_bf16(v.x, v.y);
 }
-__device__ __forceinline__ void decode16(uint8_t* slot, int key, int lane8, const uint4& c, float sc) {
-  uint8_t* blk = slot + (lane8 >> 2) * 8192;
-  const uint4 v[2] = {make_uint4(decode2(c.x, sc), decode2(c.x >> 16, sc), decode2(c.y, sc), decode2(c.y >> 16, sc)),
-                      make_uint4(decode2(c.z, sc), decode2(c.z >> 16, sc), decode2(c.w, sc), decode2(c.w >> 16, sc))};
-  // the upper four lanes of a key write another 64-dim block, in the same
-  // banks: they take their two chunks in the other order
-  const bool sw = lane8 & 4;
-  const uint32_t c0 = 2 * (lane8 & 3);
-  *reinterpret_cast<uint4*>(blk + sw128_offset(key, c0 + sw)) = sw ? v[1] : v[0];
-  *reinterpret_cast<uint4*>(blk + sw128_offset(key, c0 + !sw)) = sw ? v[0] : v[1];
+__device__ __forceinline__ uint4 decode8(uint32_t a, uint32_t b, float sc) {
+  return make_uint4(decode2(a, sc), decode2(a >> 16, sc), decode2(b, sc), decode2(b >> 16, sc));
+}
+struct Codes {
+  uint4 c;
+  float sc;
+};
+// 16 codes of a key's group (lane8: which), none where the key does not exist.
+// The upper four lanes of a key write another 64-dim block than the lower
+// four, in the same banks: they hold and store their two 16-byte chunks in the
+// other order.
+__device__ __forceinline__ Codes fetch16(const uint8_t* row, int group, int lane8, bool exists) {
+  Codes v{make_uint4(0u, 0u, 0u, 0u), 0.f};
+  if (exists) {
+    // volatile: issued here, ahead of the waits, not where the values are used
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.c.x), "=r"(v.c.y), "=r"(v.c.z), "=r"(v.c.w)
+                 : "l"(row + 128 * group + 16 * lane8));
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v.sc) : "l"(row + kDv + 4 * group));
+  }
+  return v;
+}
+struct Decoded {
+  uint4 first, second;
+};
+__device__ __forceinline__ Decoded decode16(const Codes& v, bool swap) {
+  return {decode8(swap ? v.c.z : v.c.x, swap ? v.c.w : v.c.y, v.sc),
+          decode8(swap ? v.c.x : v.c.z, swap ? v.c.y : v.c.w, v.sc)};
 }
 
 // The run of this pair: every CTA sums the requests' steps itself. `scratch`
@@ -284,8 +333,7 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Bars* s, uint8_t*
     if (b < p.B) {
       r = load_request(p, b);
       if (r.uneven && r.q_len > 0 && pair == 0) {
-        const int64_t sl = r.c + r.q_len;
-        if (sl > r.kv_len || r.c < 0) report(p.dev_status, DSA_DEVERR_SEQ_LEN);
+        report(p.dev_status, DSA_DEVERR_SEQ_LEN);
       }
       w = steps_before(p, r, r.n_tiles);
     }
@@ -373,14 +421,15 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      for (int k = 0; k < 4; ++k) mbar_init(&s->full[i][k], F8 ? 2 * kKeyWarpsF8 : 1);
-      for (int k = 0; k < 2; ++k) mbar_init(&s->other[i][k], F8 ? kOtherWarpsF8 : 1);
+      for (int k = 0; k < 4; ++k) mbar_init(&s->full[i][k], F8 ? 2 * kDecodeWarps : 1);
+      for (int k = 0; k < 2; ++k) mbar_init(&s->other[i][k], F8 ? kDecodeWarps : 1);
       mbar_init(&s->s_half[i], 1);
       mbar_init(&s->pv_half[i], 1);
       mbar_init(&s->s_full[i], 1);
       mbar_init(&s->pv_done[i], 1);
       mbar_init(&s->rows[i], 4);
     }
+    mbar_init(&s->first, 1);
     mbar_init(&s->rope, 1);
     mbar_init(&s->q, 1);
     mbar_init(&s->p_full, 16);
@@ -411,89 +460,103 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
   // a barrier's address in the even CTA
   const auto even = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
 
-  if (F8 && warp >= kOtherWarp) {
-    // ---------------- fp8: each step's other keys, as soon as S no longer
-    // needs the dims they replace; 16 keys per warp, two groups
-    const int lane8 = lane & 7, key0 = (warp - kOtherWarp) * 16 + (lane >> 3);
+  if (F8 && warp >= kKeyWarp) {
+    // ---------------- fp8: the own keys of each step, 8 per warp, two groups
+    // (slots) at a time, the next two in flight; then the other keys of the
+    // step before, as soon as S no longer needs the dims they replace
+    const int lane8 = lane & 7, key = (warp - kKeyWarp) * 8 + (lane >> 3);  // and key + 4
+    const bool swap = lane8 & 4;
+    // the two chunks of key (key + 4: 4 rows and a flipped chunk bit further)
+    const uint32_t blk = (lane8 >> 2) * 8192, c0 = 2 * (lane8 & 3);
+    const uint32_t at[2][2] = {{blk + sw128_offset(key, c0 + swap), blk + sw128_offset(key, c0 + !swap)},
+                               {blk + sw128_offset(key + 4, c0 + swap), blk + sw128_offset(key + 4, c0 + !swap)}};
+    const auto store = [&](uint8_t* slot, int i, const Decoded& v) {
+      *reinterpret_cast<uint4*>(slot + at[i][0]) = v.first;
+      *reinterpret_cast<uint4*>(slot + at[i][1]) = v.second;
+    };
+    const uint32_t full0 = even(&s->full[0][0]), other0 = even(&s->other[0][r ^ 1]);
     Cursor c;
-    int it = 0;
-    bool ok = true;
-    for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
-      for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
-        const int buf = it & 1;
-        const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + (r ^ 1), false);
-        uint4 code[4][2];
-        float2 sc[4];
+    bool more = c.start(p, s), ok = true;
+    int kt = c.k0;
+    Codes own[2][2], oth[2][2];  // [key][group]
+    Rows x{0, 0}, xo{0, 0};
+    Units u;
+    const bool rep = warp == kKeyWarp && r == 0;
+    const auto locate = [&] {
+      if (kt == c.k0) u.start(p, c, lane, rep);
+      const Rows a = u.get(p, c, 2 * kt, lane, rep), b = u.get(p, c, 2 * kt + 1, lane, rep);
+      x = r ? b : a;
+      xo = r ? a : b;
+    };
+    const auto fetch_own = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          code[i][0] = code[i][1] = make_uint4(0u, 0u, 0u, 0u);
-          sc[i] = make_float2(0.f, 0.f);
-          if (key0 + 4 * i < x.n) {
-            const uint8_t* src = p.kv + static_cast<int64_t>(x.row + key0 + 4 * i) * kF8Row;
-            code[i][0] = __ldg(reinterpret_cast<const uint4*>(src + 256 * r) + lane8);
-            code[i][1] = __ldg(reinterpret_cast<const uint4*>(src + 256 * r + 128) + lane8);
-            sc[i] = __ldg(reinterpret_cast<const float2*>(src + kDv) + r);
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* row = p.kv + static_cast<int64_t>(x.row + key + 4 * i) * kF8Row;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) own[i][g] = fetch16(row, 2 * h + g, lane8, key + 4 * i < x.n);
+      }
+    };
+    const auto fetch_other = [&](const Rows& xo) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* row = p.kv + static_cast<int64_t>(xo.row + key + 4 * i) * kF8Row;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) oth[i][g] = fetch16(row, 2 * r + g, lane8, key + 4 * i < xo.n);
+      }
+    };
+    if (more) {
+      locate();
+      fetch_own(0);
+    }
+    const auto all = [](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
+    for (int it = 0; ok && (more || it > 0); ++it) {
+      const int buf = it & 1, b1 = buf ^ 1;
+      const bool last = !more;  // only the other keys of the last step are left
+      const Rows xo_now = xo;
+      int h = last ? 2 : 0;
+      bool other_left = it > 0;
+      long long idle_since = clock64();
+#pragma unroll 1
+      while (h < 2 || other_left) {  // whichever may be stored; the other keys are waited for more urgently
+        if (other_left && all(mbar_test_wait(r ? &s->s_half[b1] : &s->s_full[b1], ((it - 1) >> 1) & 1))) {
+          uint8_t* slot = smem + kSmKv + (b1 * 4 + 2 * (r ^ 1)) * kSlot;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(oth[i][g], swap));
           }
-        }
-        if (!warp_wait(r ? &s->s_half[buf] : &s->s_full[buf], (it >> 1) & 1)) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_relaxed(other0 + b1 * 16);
+          other_left = false;
+        } else if (h < 2 && (it < 2 || all(mbar_test_wait(h == 0 ? &s->pv_half[buf] : &s->pv_done[buf],
+                                                          ((it >> 1) - 1) & 1)))) {
+          uint8_t* slot = smem + kSmKv + (buf * 4 + 2 * h) * kSlot;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(own[i][g], swap));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane < 2) mbar_arrive_remote_relaxed(full0 + (buf * 4 + 2 * h + lane) * 8);
+          ++h;
+          if (h == 2) {
+            if (++kt == c.k1) {
+              more = c.next(p);
+              kt = c.k0;
+            }
+            if (more) locate();
+          }
+          if (h == 1 || more) fetch_own(h & 1);
+        } else if (all(clock64() - idle_since > kWaitLimitCycles)) {
           if (lane == 0) abort_now();
           ok = false;
           break;
         }
-        uint8_t* slot = smem + kSmKv + (buf * 4 + 2 * (r ^ 1)) * kSlot;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          decode16(slot, key0 + 4 * i, lane8, code[i][0], sc[i].x);
-          decode16(slot + kSlot, key0 + 4 * i, lane8, code[i][1], sc[i].y);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote_relaxed(even(&s->other[buf][r ^ 1]));
       }
-    }
-  } else if (F8 && warp >= kKeyWarp) {
-    // ---------------- fp8: the own keys of each step; 8 keys per warp, loaded
-    // before the step's slots come free
-    const int lane8 = lane & 7, key0 = (warp - kKeyWarp) * 8 + (lane >> 3);
-    Cursor c;
-    int it = 0;
-    bool ok = true;
-    for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
-      for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
-        const int buf = it & 1;
-        const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + r, warp == kKeyWarp && lane == 0);
-        uint4 code[2][4];
-        float4 sc[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) code[i][k] = make_uint4(0u, 0u, 0u, 0u);
-          sc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (key0 + 4 * i < x.n) {
-            const uint8_t* src = p.kv + static_cast<int64_t>(x.row + key0 + 4 * i) * kF8Row;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) code[i][k] = __ldg(reinterpret_cast<const uint4*>(src + 128 * k) + lane8);
-            sc[i] = __ldg(reinterpret_cast<const float4*>(src + kDv));
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (it >= 2 && (k & 1) == 0 && !warp_wait(k == 0 ? &s->pv_half[buf] : &s->pv_done[buf], ((it >> 1) - 1) & 1)) {
-            if (lane == 0) abort_now();
-            ok = false;
-            break;
-          }
-          uint8_t* slot = smem + kSmKv + (buf * 4 + k) * kSlot;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            decode16(slot, key0 + 4 * i, lane8, code[i][k],
-                     k == 0 ? sc[i].x : k == 1 ? sc[i].y : k == 2 ? sc[i].z : sc[i].w);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote_relaxed(even(&s->full[buf][k]));
-        }
-        if (!ok) break;
-      }
+      if (last) break;
+      fetch_other(xo_now);
     }
   } else if (warp == kKeyWarp) {
     // ---------------- the own keys of each step, all 512 latent dims
@@ -501,9 +564,17 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
     int it = 0;
     bool ok = true;
     for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
+      Units u;
+      u.start(p, c, lane, true);
       for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
         const int buf = it & 1;
-        const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + r, lane == 0);
+        const Rows x = u.get(p, c, 2 * kt + r, lane, true);
+        // copies are served in order: the second step's wait for what the first S needs
+        if (it == 1 && !warp_wait(&s->first, 0)) {
+          if (lane == 0) abort_now();
+          ok = false;
+          break;
+        }
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
           if (it >= 2 && (k & 1) == 0 && !warp_wait(k == 0 ? &s->pv_half[buf] : &s->pv_done[buf], ((it >> 1) - 1) & 1)) {
@@ -548,21 +619,37 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
       if (!ok && lane == 0) abort_now();
       return ok;
     };
+    const auto load_q = [&](int row0) {  // this CTA's 64 rows of the row tile
+      if (lane == 0) {
+        if (r == 0) mbar_arrive_expect_tx(&s->q, 2 * 9 * 8192);
+        tma_load_3d_pair(smem_u32(smem + kSmQ), &qmap, even(&s->q), 0, row0 + 64 * r, 0);
+      }
+      __syncwarp();
+    };
     for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
+      const int row0 = (c.req.q0 + c.tile * p.tpt) * p.H;
+      if (it == 0) load_q(row0);  // needs nothing else: ahead of the block table's entries
+      Units u;
+      u.start(p, c, lane, false);
+      // fp8: the decoding warps' loads are short of registers to run far ahead
+      // in; the own keys of the step kAhead further on are asked into L2
+      Units far = u;
+      const auto ask = [&](int kt) {
+        const Rows x = far.get(p, c, 2 * kt + r, lane, false);
+        if (x.n > 0 && lane == 0) prefetch_l2(p.kv + static_cast<int64_t>(x.row) * kF8Row, x.n * kF8Row);
+      };
+      for (int kt = c.k0; F8 && kt < min(c.k0 + kAhead, c.k1); ++kt) ask(kt);
       for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
-        const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + r, false);
-        const Rows next_other = rows_of(p, c.b, c.req.kv_len, 2 * kt + (r ^ 1), false);
+        if (F8 && kt + kAhead < c.k1) ask(kt + kAhead);
+        const Rows a = u.get(p, c, 2 * kt, lane, false), b = u.get(p, c, 2 * kt + 1, lane, false);
+        const Rows x = r ? b : a, next_other = r ? a : b;
         if (it >= 1 && !after_s(it - 1)) break;
         if (r == 0 && lane == 0) mbar_arrive_expect_tx(&s->rope, 2 * 8192);
         load_keys(smem_u32(smem + kSmRope), &ropemap, &rowmap, even(&s->rope), x, p.total_rows, F8 ? 0 : 8, 1,
                   lane);
+        if (!F8 && it == 0 && lane == 0) mbar_arrive(&s->first);
         if (!F8 && it >= 1 && r == 0) load_other(it - 1);
-        if (kt == c.k0 && lane == 0) {
-          if (r == 0) mbar_arrive_expect_tx(&s->q, 2 * 9 * 8192);
-          const int row0 = (c.req.q0 + c.tile * p.tpt) * p.H + 64 * r;
-          tma_load_3d_pair(smem_u32(smem + kSmQ), &qmap, even(&s->q), 0, row0, 0);
-        }
-        __syncwarp();
+        if (it >= 1 && kt == c.k0) load_q(row0);
         other = next_other;
       }
     }
@@ -581,13 +668,14 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
       const uint64_t dv = smem_desc(smem_u32(smem), 8192, 1024, kSwizzle128B);
       const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
       const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
-      Cursor cq, cp;
-      bool more_q = cq.start(p, s), more_p = cp.start(p, s);
+      Cursor c;
+      bool more = c.start(p, s);
       int iq = 0, ip = 0, sub = 0, half = 0, segs = 0;  // the next S and PV, and the parts of them
-      int kq = cq.k0, kp = cp.k0;
+      int kt = c.k0;
+      uint32_t first = 0;  // bit i & 1: step i begins a segment
       const auto all = [](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
       long long idle_since = clock64();
-      while (more_p && !__any_sync(0xFFFFFFFFu, s->abort)) {
+      while ((more || ip < iq) && !__any_sync(0xFFFFFFFFu, s->abort)) {
         bool progressed = false;
         if (ip < iq && all(half == 0 ? mbar_test_wait(&s->p_full, ip & 1) && mbar_test_wait(&s->other[ip & 1][0], (ip >> 1) & 1)
                                      : mbar_test_wait(&s->other[ip & 1][1], (ip >> 1) & 1))) {
@@ -595,7 +683,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
           const int buf = ip & 1;
           const uint32_t a0 = k_lo + ((kSmP + half * 8192) >> 4);
           const uint32_t b0 = v_lo + ((kSmKv + (buf * 4 + 2 * half) * kSlot) >> 4);
-          const uint32_t acc0 = (kp > cp.k0 || half) ? 1u : 0u;
+          const uint32_t acc0 = half ? 1u : ~(first >> buf) & 1u;
           if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {  // 16 keys each
@@ -607,20 +695,14 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
             mma_commit_pair(half ? &s->pv_done[buf] : &s->pv_half[buf]);
           }
           __syncwarp();
-          if (half) {
-            ++ip;
-            if (++kp == cp.k1) {
-              more_p = cp.next(p);
-              kp = cp.k0;
-            }
-          }
+          ip += half;
           half ^= 1;
           progressed = true;
         }
-        if (more_q && iq < ip + 2) {  // PV of step iq - 2 has been issued: S was read
+        if (more && iq < ip + 2) {  // PV of step iq - 2 has been issued: S was read
           const int buf = iq & 1;
           bool ready = sub < 4 ? mbar_test_wait(&s->full[buf][sub], (iq >> 1) & 1) : mbar_test_wait(&s->rope, iq & 1);
-          if (sub == 0 && kq == cq.k0) ready = ready && mbar_test_wait(&s->q, segs & 1);
+          if (sub == 0 && kt == c.k0) ready = ready && mbar_test_wait(&s->q, segs & 1);
           if (all(ready)) {
             tc_fence_after();
             const uint32_t d = tmem + kColS + 64 * buf;
@@ -644,12 +726,13 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
                                    k_lo + ((kSmRope + st * 32) >> 4), k_hi, idesc_qk, 1u);
                 mma_commit_pair(&s->s_full[buf]);
               }
+              first = (first & ~(1u << buf)) | (kt == c.k0 ? 1u << buf : 0u);
               sub = 0;
               ++iq;
-              if (++kq == cq.k1) {
+              if (++kt == c.k1) {
                 ++segs;
-                more_q = cq.next(p);
-                kq = cq.k0;
+                more = c.next(p);
+                kt = c.k0;
               }
             }
             __syncwarp();
@@ -661,7 +744,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp < kAuxWarp) {
     // ---------------- softmax: TMEM lane = 32 (warp % 4) + lane holds row
     // lane % 64 against the keys of CTA lane / 64; the two warps of a lane
     // group take 32 keys (and 128 columns of O) each
@@ -689,9 +772,11 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
       const bool live = in_tile < p.tpt * p.H && tok < c.req.q_len;
       const int lim = live ? visible(c.req, tok) : 0;
       float m = kNegSentinel, l = 0.f;
+      Units u;
+      u.start(p, c, lane, false);
       for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
         const int buf = it & 1;
-        const Rows x = rows_of(p, c.b, c.req.kv_len, 2 * kt + kh, false);
+        const Rows x = u.get(p, c, 2 * kt + kh, lane, false);
         const int n = x.n == 0 ? 0 : lim - kt * kTile - kh * 64 - half * 32;  // of this thread's 32 keys, visible ones
         if (!warp_wait(&s->s_full[buf], (it >> 1) & 1)) {
           if (lane == 0) abort_now();
@@ -817,7 +902,8 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
         if (kh == 0 && half == 0) p.ml_part[slot * 128 + in_tile] = make_float2(m, l);
         if (c.k0 == 0 && r == 0 && tid == 0) {
           // pairs whose runs hold the rest of this row tile
-          const int last = static_cast<int>((c.pos + c.nk - 1) / s->per);
+          const int64_t at = s->end - c.left;
+          const int last = static_cast<int>((at + c.nk - 1) / s->per);
           const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt) - c.tile * p.tpt) * p.H;
           p.desc[pair] = make_int4((c.req.q0 + c.tile * p.tpt) * p.H, rows, last - pair, 0);
         }
