@@ -64,10 +64,17 @@ class DsaStep:
 
     num_kv_splits: 0 automatic, -1 batch-invariant (fixed by index_topk), n > 0
     that many; when 0 and the environment sets DSA_NUM_KV_SPLITS, that value.
+    dense: attention over all keys instead (no indexer, no top-k), as for
+    requests not longer than index_topk; num_kv_splits is then 0 (keys spread
+    over the GPU), 1 or -1 (never cut), and DSA_NUM_KV_SPLITS does not count.
     DSA_NVTX=1 wraps each call in an NVTX range (for profilers)."""
 
-    def __init__(self, wl, device="cuda", num_kv_splits: int = 0, prefill: bool | None = None, kv_fp8: bool = False):
-        if num_kv_splits == 0 and os.environ.get("DSA_NUM_KV_SPLITS"):
+    def __init__(self, wl, device="cuda", num_kv_splits: int = 0, prefill: bool | None = None, kv_fp8: bool = False,
+                 dense: bool = False):
+        self.dense = dense
+        if dense and num_kv_splits not in (0, 1, api.DSA_KV_SPLITS_BATCH_INVARIANT):
+            raise ValueError(f"dense attention takes num_kv_splits 0, 1 or -1, got {num_kv_splits}")
+        if not dense and num_kv_splits == 0 and os.environ.get("DSA_NUM_KV_SPLITS"):
             num_kv_splits = int(os.environ["DSA_NUM_KV_SPLITS"])
         self.nvtx = _nvtx_enabled()
         self.wl = wl
@@ -101,10 +108,14 @@ class DsaStep:
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=d)
         self.prefill = (wl.max_q_len > 2) if prefill is None else prefill
         # num_kv_splits: 0 automatic, -1 batch-invariant (fixed by index_topk), n > 0 that many
-        self.splits = 1 if self.prefill else api.sparse_mla_num_splits(wl.T, wl.H, wl.Dv, wl.index_topk,
-                                                                         num_kv_splits)
+        if dense:
+            self.splits = num_kv_splits
+            ws_mla = api.dense_mla_workspace_size(wl.T, wl.H, wl.Dv, num_kv_splits)
+        else:
+            self.splits = 1 if self.prefill else api.sparse_mla_num_splits(wl.T, wl.H, wl.Dv, wl.index_topk,
+                                                                             num_kv_splits)
+            ws_mla = api.sparse_mla_workspace_size(wl.T, wl.H, wl.Dv, self.splits)
         ws_topk = api.dsa_topk_workspace_size(wl.T, wl.ld, wl.index_topk)
-        ws_mla = api.sparse_mla_workspace_size(wl.T, wl.H, wl.Dv, self.splits)
         self.ws_topk = torch.empty(max(ws_topk, 16), dtype=torch.uint8, device=d)
         self.ws_mla = torch.empty(max(ws_mla, 16), dtype=torch.uint8, device=d)
 
@@ -120,7 +131,7 @@ class DsaStep:
             self._topk(stream)
 
     def attention(self, stream=None):
-        with self._range("sparse_mla"):
+        with self._range("dense_mla" if self.dense else "sparse_mla"):
             self._attention(stream)
 
     def _indexer(self, stream=None):
@@ -133,6 +144,11 @@ class DsaStep:
 
     def _attention(self, stream=None):
         wl = self.wl
+        if self.dense:
+            dense = api.dense_mla_attention_fp8 if self.kv_fp8 else api.dense_mla_attention
+            dense(self.q, self.kv_cache, self.block_table, self.seq_lens, self.qsl, wl.softmax_scale, wl.Dv, self.out,
+                  self.lse, self.splits, self.ws_mla, self.dev_status, stream)
+            return
         prefill = api.sparse_mla_prefill_fp8 if self.kv_fp8 else api.sparse_mla_prefill
         decode = api.sparse_mla_decode_fp8 if self.kv_fp8 else api.sparse_mla_decode
         if self.prefill:
@@ -143,8 +159,9 @@ class DsaStep:
                    wl.Dv, self.out, self.lse, self.splits, self.ws_mla, self.dev_status, stream)
 
     def run(self, stream=None):
-        self.indexer(stream)
-        self.topk(stream)
+        if not self.dense:
+            self.indexer(stream)
+            self.topk(stream)
         self.attention(stream)
         return self.out
 
@@ -163,8 +180,9 @@ class DsaStep:
             self.inputs_q.copy_(host_q, non_blocking=True)
             self._q_copied.record(self._side)
         self.inputs.copy_(host_inputs, non_blocking=True)
-        self.indexer()
-        self.topk()
+        if not self.dense:
+            self.indexer()
+            self.topk()
         main.wait_event(self._q_copied)
         self.attention()
         host_outputs.copy_(self.outputs, non_blocking=True)
@@ -172,6 +190,8 @@ class DsaStep:
 
     def kernel_launches(self) -> int:
         """Kernels one run() enqueues."""
+        if self.dense:
+            return 2 if self.splits == 0 else 1
         n = 1  # indexer
         n += 2 if api.dsa_topk_workspace_size(self.wl.T, self.wl.ld, self.wl.index_topk) else 1
         n += 1 if (self.prefill or self.splits == 1) else 2
