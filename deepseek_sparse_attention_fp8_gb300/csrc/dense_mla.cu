@@ -24,23 +24,15 @@
 // Work: the steps of all row tiles form one sequence, cut into equal runs, one
 // per CTA pair (one persistent wave). A row tile cut by a run's end leaves
 // fp32 partials, at most two per pair, joined by dense_mla_merge_kernel.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <algorithm>
-#include <cmath>
 
-#include "common.cuh"
-#include "ptx.cuh"
+#include "dense_mla.cuh"
 
 namespace dsa {
 namespace {
 
-using namespace ptx;
+using namespace dense;
 
-constexpr int kDk = 576, kDv = 512, kF8Row = 656;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // Warps 0-7 softmax, 8 q / rope (bf16 cache: and the other keys), 9 MMA, then
 // the own keys: one warp of TMA copies, or (fp8 cache) 8 decoding warps, which
@@ -49,12 +41,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kAuxWarp = 8, kMmaWarp = 9, kKeyWarp = 10, kDecodeWarps = 8;
 template <bool F8>
 constexpr int kThreadsOf = 32 * (kKeyWarp + (F8 ? kDecodeWarps : 1));
-constexpr int kTile = 128;
-constexpr int kSlot = 16384;  // 64 keys x 128 dims
-constexpr float kRescaleThreshold = 8.f;  // log2 units
-constexpr long long kWaitLimitCycles = 2000000000ll;
 constexpr int kAhead = 3;   // steps (fp8 cache)
-constexpr int kMinRun = 4;  // steps a run has at least when row tiles may be cut
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;  // O 256 columns, S 2 x 64
 
 // Shared memory: q as 9 blocks of 64 rows x 64 dims, two steps of 4 key slots,
@@ -77,330 +64,9 @@ struct Bars {
   uint64_t first;        // q and the rope dims of the run's first step have been asked for
   uint32_t tmem;
   volatile int abort;
-  // the run: first request, row tile and step of it, and the units [pos, end)
-  int32_t b, tile, k0, pad;
-  int64_t pos, end, per, total;
+  Run run;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block too large");
-
-struct DenseParams {
-  int32_t num_blocks, rows_per_block, total_rows;
-  const int32_t* block_table;
-  int32_t bt_stride;
-  const int32_t *seq_lens, *qsl;
-  int32_t B, T, H, tpt;      // tpt: tokens per row tile
-  int32_t block_size, bs64;  // bs64 = block_size / 64
-  float scale_log2;
-  const uint8_t* kv;  // the fp8 cache
-  int32_t cut;    // row tiles may be cut
-  int32_t out32;  // out is 32-byte aligned
-  uint16_t* out;
-  float* lse;
-  float4* o_part;   // [2 per pair][2 CTAs][64 column groups][128 lanes]
-  float2* ml_part;  // [2 per pair][128 rows]: max (log2 units), sum
-  int4* desc;       // per pair: the cut row tile that starts in its run
-  int32_t* dev_status;
-};
-
-// A request's rows as work: row tile i has steps(i) = max(1, ceil(keys its
-// last token sees / 128)).
-struct Request {
-  int32_t q0, q_len, n_tiles, kv_len;  // kv_len: its cached keys that the table can hold
-  int32_t c;     // position of its first new token (a length below 0 counts as 0)
-  bool uneven;   // lengths that contradict each other: every tile is charged kv_len
-};
-
-__device__ __forceinline__ Request load_request(const DenseParams& p, int b) {
-  Request r;
-  const int q0 = min(max(__ldg(p.qsl + b), 0), p.T), q1 = min(max(__ldg(p.qsl + b + 1), 0), p.T);
-  const int64_t sl = __ldg(p.seq_lens + b), cap = static_cast<int64_t>(p.bt_stride) * p.block_size;
-  r.q0 = q0;
-  r.q_len = max(q1 - q0, 0);
-  r.n_tiles = (r.q_len + p.tpt - 1) / p.tpt;
-  // at most 2^31 - 256, so that sums of a few steps stay within 31 bits
-  r.kv_len = static_cast<int32_t>(max(int64_t(0), min(min(sl, cap), int64_t(0x7FFFFF00))));
-  r.c = static_cast<int32_t>(max(sl, int64_t(0))) - r.q_len;
-  r.uneven = r.c < 0 || r.kv_len != sl;
-  return r;
-}
-// keys visible to the token i (from 0) of the request
-__device__ __forceinline__ int visible(const Request& r, int i) {
-  return max(0, min(r.c + i + 1, r.kv_len));
-}
-__device__ __forceinline__ int steps_of(const DenseParams& p, const Request& r, int tile) {
-  const int keys = r.uneven ? r.kv_len : visible(r, min(r.q_len, (tile + 1) * p.tpt) - 1);
-  return max(1, (keys + kTile - 1) / kTile);
-}
-// sum over i < n of floor((a i + b) / 128)
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
-  if ((a & (a - 1)) == 0) {  // a divides 128: floor((i + b / a) / (128 / a)), a whole run of each quotient
-    const int sh = 7 - (31 - __clz(static_cast<int>(a)));
-    const auto upto = [&](int64_t x) {  // sum over j < x of floor(j / 2^sh)
-      const int64_t k = x >> sh;
-      return ((k * (k - 1) / 2) << sh) + k * (x & ((int64_t(1) << sh) - 1));
-    };
-    const int64_t b0 = b / a;
-    return upto(n + b0) - upto(b0);
-  }
-  // the lattice points under the line, by the Euclidean algorithm
-  int64_t sum = 0, m = 128;
-  while (true) {
-    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const int64_t top = a * n + b;
-    if (top < m) return sum;
-    n = top / m;
-    b = top % m;
-    const int64_t t = m;
-    m = a;
-    a = t;
-  }
-}
-// steps of the request's row tiles before tile n
-__device__ __forceinline__ int64_t steps_before(const DenseParams& p, const Request& r, int n) {
-  if (r.uneven) return static_cast<int64_t>(n) * steps_of(p, r, 0);
-  if (n == 0) return 0;
-  if (n < r.n_tiles) return floor_sum(n, p.tpt, static_cast<int64_t>(r.c) + p.tpt + kTile - 1);
-  return floor_sum(n - 1, p.tpt, static_cast<int64_t>(r.c) + p.tpt + kTile - 1) + steps_of(p, r, n - 1);
-}
-
-// A run of steps, segment by segment (a segment: the steps of one row tile).
-struct Cursor {
-  Request req;
-  int32_t b, tile, nk, k0, k1;
-  int32_t left;  // steps of the run from this segment on
-  __device__ __forceinline__ void cut(const DenseParams& p) {
-    nk = steps_of(p, req, tile);
-    k1 = p.cut ? min(nk, k0 + left) : nk;
-  }
-  __device__ __forceinline__ bool start(const DenseParams& p, const Bars* s) {
-    b = s->b;
-    tile = s->tile;
-    k0 = k1 = nk = s->k0;
-    left = static_cast<int32_t>(s->end - s->pos);
-    if (left <= 0) return false;
-    req = load_request(p, b);
-    cut(p);
-    return true;
-  }
-  __device__ __forceinline__ bool next(const DenseParams& p) {
-    left -= k1 - k0;
-    if (left <= 0) return false;
-    k0 = 0;
-    if (++tile >= req.n_tiles) {
-      tile = 0;
-      do {
-        if (++b >= p.B) return false;
-        req = load_request(p, b);
-      } while (req.n_tiles == 0);
-    }
-    cut(p);
-    return true;
-  }
-};
-
-// The cache rows of a unit of 64 keys: their first row (total_rows, which
-// reads as zeros, where there is none) and how many of them exist.
-struct Rows {
-  int32_t row, n;
-};
-// A warp's view of a row tile's part of the block table: lane l holds the
-// entry of unit base + l, and the entries of the 32 units behind are in flight,
-// so that no step waits for the table. Called by whole warps.
-struct Units {
-  int32_t base, row, ahead;
-  __device__ __forceinline__ int32_t entry(const DenseParams& p, const Cursor& c, int unit) const {
-    const int64_t key = static_cast<int64_t>(unit) * 64;
-    return key < c.req.kv_len ? __ldg(p.block_table + static_cast<int64_t>(c.b) * p.bt_stride + unit / p.bs64) : 0;
-  }
-  __device__ __forceinline__ int32_t first_row(const DenseParams& p, const Cursor& c, int32_t blk, int unit, bool rep) const {
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (rep && static_cast<int64_t>(unit) * 64 < c.req.kv_len) report(p.dev_status, DSA_DEVERR_BLOCK_OOB);
-      return -1;
-    }
-    return blk * p.rows_per_block + (unit % p.bs64) * 64;
-  }
-  __device__ __forceinline__ void start(const DenseParams& p, const Cursor& c, int lane, bool rep) {
-    base = 2 * c.k0;
-    row = entry(p, c, base + lane);
-    ahead = entry(p, c, base + 32 + lane);
-    row = first_row(p, c, row, base + lane, rep);
-  }
-  // units are asked for in ascending order, at most 32 behind the last
-  __device__ __forceinline__ Rows get(const DenseParams& p, const Cursor& c, int unit, int lane, bool rep) {
-    if (unit >= base + 32) {
-      base += 32;
-      row = first_row(p, c, ahead, base + lane, rep);
-      ahead = entry(p, c, base + 32 + lane);
-    }
-    const int left = c.req.kv_len - unit * 64;
-    const int32_t first = __shfl_sync(0xFFFFFFFFu, row, (unit - base) & 31);
-    if (left <= 0 || first < 0) return {p.total_rows, 0};
-    return {first, min(left, 64)};
-  }
-};
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-// mbar_wait with one answer for the warp
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
-}
-
-// Loads 64 keys x 64 * blocks dims (dim block d0 on) by the whole warp. The
-// rows behind a request's last key are not its own and may hold anything,
-// NaN included, so they are gathered from past the cache's end, as zeros.
-__device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* box, const CUtensorMap* row_map,
-                                          uint32_t bar, Rows x, int32_t total_rows, int d0, int blocks, int lane) {
-  if (x.n == 0 || x.n == 64) {
-    if (lane == 0) tma_load_3d_pair(dst, box, bar, 0, x.row, d0);
-  } else {
-    const int g = lane & 15, d = lane >> 4;
-    if (d < blocks) {
-      int r[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = 4 * g + i < x.n ? x.row + 4 * g + i : total_rows;
-      tma_gather4_pair(dst + d * 8192 + g * 512, row_map, bar, (d0 + d) * 64, r[0], r[1], r[2], r[3]);
-    }
-  }
-  __syncwarp();
-}
-
-// ---- fp8 cache: a row's 128 codes of one group are 8 lanes' 16 bytes, read
-// straight into registers, decoded (code * scale in fp32, rounded to bf16:
-// the tensor cores take bf16) and stored as the swizzled tile the copies of
-// the bf16 cache would bring.
-__device__ __forceinline__ float2 mul2(float2 a, float s) {  // two products in one instruction
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmul.rn.f32x2 c, a, b;\n\t"
-      "mov.b64 {%0, %1}, c;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(s));
-  return r;
-}
-__device__ __forceinline__ uint32_t decode2(uint32_t two, float sc) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  const float2 v = mul2(f, sc);
-  return pack_bf16(v.x, v.y);
-}
-__device__ __forceinline__ uint4 decode8(uint32_t a, uint32_t b, float sc) {
-  return make_uint4(decode2(a, sc), decode2(a >> 16, sc), decode2(b, sc), decode2(b >> 16, sc));
-}
-struct Codes {
-  uint4 c;
-  float sc;
-};
-// 16 codes of a key's group (lane8: which), none where the key does not exist.
-// The upper four lanes of a key write another 64-dim block than the lower
-// four, in the same banks: they hold and store their two 16-byte chunks in the
-// other order.
-__device__ __forceinline__ Codes fetch16(const uint8_t* row, int group, int lane8, bool exists) {
-  Codes v{make_uint4(0u, 0u, 0u, 0u), 0.f};
-  if (exists) {
-    // volatile: issued here, ahead of the waits, not where the values are used
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.c.x), "=r"(v.c.y), "=r"(v.c.z), "=r"(v.c.w)
-                 : "l"(row + 128 * group + 16 * lane8));
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v.sc) : "l"(row + kDv + 4 * group));
-  }
-  return v;
-}
-struct Decoded {
-  uint4 first, second;
-};
-__device__ __forceinline__ Decoded decode16(const Codes& v, bool swap) {
-  return {decode8(swap ? v.c.z : v.c.x, swap ? v.c.w : v.c.y, v.sc),
-          decode8(swap ? v.c.x : v.c.z, swap ? v.c.y : v.c.w, v.sc)};
-}
-
-// The run of this pair: every CTA sums the requests' steps itself. `scratch`
-// is shared memory that nothing else uses yet.
-template <int kThreads>
-__device__ __forceinline__ void plan_run(const DenseParams& p, Bars* s, uint8_t* scratch, int pair, int n_pairs) {
-  int64_t* sums = reinterpret_cast<int64_t*>(scratch);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kWarps = kThreads / 32;
-  const bool once = p.B <= kThreads;
-  int64_t w = 0, incl = 0;
-  Request r = {};
-  const auto scan = [&](int b) {  // steps of request b, and their inclusive sum over the block's requests
-    w = 0;
-    if (b < p.B) {
-      r = load_request(p, b);
-      if (r.uneven && r.q_len > 0 && pair == 0) {
-        report(p.dev_status, DSA_DEVERR_SEQ_LEN);
-      }
-      w = steps_before(p, r, r.n_tiles);
-    }
-    incl = w;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-      if (lane >= off) incl += u;
-    }
-    __syncthreads();
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    int64_t all = 0;
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) incl += sums[i];
-      all += sums[i];
-    }
-    return all;
-  };
-  int64_t total = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) total += scan(b0 + tid);
-  int64_t per = (total + n_pairs - 1) / n_pairs;
-  if (p.cut) per = max(per, int64_t(kMinRun));
-  const int64_t u0 = per * pair, u1 = min(u0 + per, total);
-  if (tid == 0) {
-    s->per = per;
-    s->total = total;
-    s->pos = s->end = 0;
-  }
-  __syncthreads();
-  if (u0 < u1) {
-    int64_t base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-      const int64_t all = once ? total : scan(b0 + tid);
-      const int64_t from = base + incl - w;
-      if (w > 0 && from <= u0 && u0 < from + w) {
-        const int64_t u = u0 - from;
-        int lo = 0, hi = r.n_tiles - 1;  // the last row tile that starts at or before u
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (steps_before(p, r, mid) <= u) lo = mid; else hi = mid - 1;
-        }
-        const int64_t at = steps_before(p, r, lo);
-        s->b = b0 + tid;
-        s->tile = lo;
-        s->k0 = static_cast<int32_t>(u - at);
-        s->pos = u0;
-        s->end = u1;
-        if (!p.cut && u > at) {  // the row tile belongs to the run it starts in: begin with the next
-          s->k0 = 0;
-          s->pos = from + steps_before(p, r, lo + 1);
-          if (lo + 1 < r.n_tiles) {
-            s->tile = lo + 1;
-          } else if (s->pos < u1) {
-            int b = b0 + tid;
-            do ++b; while (load_request(p, b).n_tiles == 0);
-            s->b = b;
-            s->tile = 0;
-          }
-        }
-      }
-      base += all;
-    }
-  }
-  fence_proxy_async_smem();  // the copies that follow write where the scratch was
-  __syncthreads();
-}
 
 template <bool F8>
 __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __grid_constant__ DenseParams p,
@@ -451,7 +117,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
   tc_fence_after();
   const uint32_t tmem = s->tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_run<kThreadsOf<F8>>(p, s, smem + kSmKv, pair, n_pairs);
+  plan_run<kThreadsOf<F8>>(p, &s->run, smem + kSmKv, pair, n_pairs);
 
   const auto abort_now = [&] {
     s->abort = 1;
@@ -476,7 +142,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
     };
     const uint32_t full0 = even(&s->full[0][0]), other0 = even(&s->other[0][r ^ 1]);
     Cursor c;
-    bool more = c.start(p, s), ok = true;
+    bool more = c.start(p, &s->run), ok = true;
     int kt = c.k0;
     Codes own[2][2], oth[2][2];  // [key][group]
     Rows x{0, 0}, xo{0, 0};
@@ -563,7 +229,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
     Cursor c;
     int it = 0;
     bool ok = true;
-    for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
+    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p)) {
       Units u;
       u.start(p, c, lane, true);
       for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
@@ -626,7 +292,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
       }
       __syncwarp();
     };
-    for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
+    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p)) {
       const int row0 = (c.req.q0 + c.tile * p.tpt) * p.H;
       if (it == 0) load_q(row0);  // needs nothing else: ahead of the block table's entries
       Units u;
@@ -669,7 +335,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
       const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
       const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
       Cursor c;
-      bool more = c.start(p, s);
+      bool more = c.start(p, &s->run);
       int iq = 0, ip = 0, sub = 0, half = 0, segs = 0;  // the next S and PV, and the parts of them
       int kt = c.k0;
       uint32_t first = 0;  // bit i & 1: step i begins a segment
@@ -766,7 +432,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
       if (lane == 0) mbar_arrive(&s->rows[warp & 1]);
       return warp_wait(&s->rows[warp & 1], meets++ & 1);
     };
-    for (bool more = c.start(p, s); more && ok; more = c.next(p)) {
+    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p)) {
       const int in_tile = 64 * r + row;  // row of the row tile
       const int tok = c.tile * p.tpt + in_tile / p.H;
       const bool live = in_tile < p.tpt * p.H && tok < c.req.q_len;
@@ -902,8 +568,8 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
         if (kh == 0 && half == 0) p.ml_part[slot * 128 + in_tile] = make_float2(m, l);
         if (c.k0 == 0 && r == 0 && tid == 0) {
           // pairs whose runs hold the rest of this row tile
-          const int64_t at = s->end - c.left;
-          const int last = static_cast<int>((at + c.nk - 1) / s->per);
+          const int64_t at = s->run.end - c.left;
+          const int last = static_cast<int>((at + c.nk - 1) / s->run.per);
           const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt) - c.tile * p.tpt) * p.H;
           p.desc[pair] = make_int4((c.req.q0 + c.tile * p.tpt) * p.H, rows, last - pair, 0);
         }
@@ -912,7 +578,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
     }
     if (p.cut && r == 0 && tid == 0 && ok) {
       // nothing to join: no row tile that starts in this run goes on behind it
-      if (s->pos >= s->end || c.k0 > 0 || c.k1 == c.nk) p.desc[pair] = make_int4(0, 0, 0, 0);
+      if (s->run.pos >= s->run.end || c.k0 > 0 || c.k1 == c.nk) p.desc[pair] = make_int4(0, 0, 0, 0);
     }
     if (p.cut && r == 0 && tid == 0 && !ok) p.desc[pair] = make_int4(0, 0, 0, 0);
   }
@@ -929,30 +595,35 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
   if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-// Joins the partials of the row tile that starts in pair blockIdx.y's run and
-// goes on behind it: out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j. A
-// thread takes 16 dims of a row, one 32-byte sector of the result.
+// Joins the partials of the row tile that starts in run blockIdx.y and goes on
+// behind it: out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j. A thread takes
+// 16 columns, i.e. dims, of a row: one 32-byte sector of the result. Partials
+// lie as the accumulators do in tensor memory: QUAD 512 columns of 128 rows per
+// CTA, else 256 columns with a row's upper dims in lane + 64.
+template <bool QUAD>
 __global__ void __launch_bounds__(128) dense_mla_merge_kernel(const __grid_constant__ DenseParams p) {
+  constexpr int kRows = QUAD ? 256 : 128, kGroups = QUAD ? 32 : 16;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int pair = blockIdx.y;
-  const int4 d = p.desc[pair];
+  const int run = blockIdx.y;
+  const int4 d = p.desc[run];
   if (d.z <= 0) return;
-  const int r = blockIdx.x >> 4, g = blockIdx.x & 15;  // CTA, 4 column groups
-  const int lane = threadIdx.x, in_tile = 64 * r + (lane & 63);
+  const int r = blockIdx.x / kGroups, g = blockIdx.x % kGroups;  // CTA, 16 columns
+  const int lane = threadIdx.x, in_tile = QUAD ? 128 * r + lane : 64 * r + (lane & 63);
+  const int dim = QUAD ? 128 * (g >> 4) + 16 * (g & 7) + ((g >> 3) & 1) * 256 : 256 * (lane >> 6) + 16 * g;
   if (in_tile >= d.y) return;
   const int parts = d.z + 1;
-  const auto slot = [&](int j) { return j == 0 ? 2 * pair + 1 : 2 * (pair + j); };
+  const auto slot = [&](int j) { return j == 0 ? 2 * run + 1 : 2 * (run + j); };
   float M = kNegSentinel;
-  for (int j = 0; j < parts; ++j) M = fmaxf(M, p.ml_part[slot(j) * 128 + in_tile].x);
+  for (int j = 0; j < parts; ++j) M = fmaxf(M, p.ml_part[slot(j) * kRows + in_tile].x);
   float den = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < parts; ++j) {
-    const float2 ml = p.ml_part[slot(j) * 128 + in_tile];
+    const float2 ml = p.ml_part[slot(j) * kRows + in_tile];
     const float w = exp2f(ml.x - M);
     den = fmaf(w, ml.y, den);
-    const float4* o = p.o_part + (static_cast<int64_t>(2 * slot(j) + r) * 64 + 4 * g) * 128 + lane;
+    const float4* o = p.o_part + (static_cast<int64_t>(2 * slot(j) + r) * (4 * kGroups) + 4 * g) * 128 + lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 v = o[i * 128];
@@ -964,18 +635,20 @@ __global__ void __launch_bounds__(128) dense_mla_merge_kernel(const __grid_const
   }
   const float inv = den > 0.f ? 1.f / den : 0.f;
   const int64_t row = static_cast<int64_t>(d.x) + in_tile;
-  uint4* dst = reinterpret_cast<uint4*>(p.out + row * kDv + 256 * (lane >> 6) + 16 * g);
+  uint4* dst = reinterpret_cast<uint4*>(p.out + row * kDv + dim);
 #pragma unroll
   for (int e = 0; e < 2; ++e)
     dst[e] = make_uint4(pack_bf16(acc[2 * e].x * inv, acc[2 * e].y * inv), pack_bf16(acc[2 * e].z * inv, acc[2 * e].w * inv),
                         pack_bf16(acc[2 * e + 1].x * inv, acc[2 * e + 1].y * inv),
                         pack_bf16(acc[2 * e + 1].z * inv, acc[2 * e + 1].w * inv));
-  if (g == 0 && lane < 64 && p.lse != nullptr) p.lse[row] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
+  if (dim == 0 && p.lse != nullptr) p.lse[row] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
-FuncAttrOnce g_smem_dense[2], g_smem_dense_merge;
+FuncAttrOnce g_smem_dense[2], g_smem_merge[2];
 
 int num_pairs() { return std::max(1, num_sms() / 2); }
+// partials of 128 rows per pair; a quad's 256 rows take two pairs' worth, and
+// there are at most half as many
 size_t o_part_bytes(int pairs) { return static_cast<size_t>(2 * pairs) * 128 * kDv * sizeof(float); }
 size_t ml_part_bytes(int pairs) { return static_cast<size_t>(2 * pairs) * 128 * sizeof(float2); }
 size_t workspace_bytes(int pairs) { return o_part_bytes(pairs) + ml_part_bytes(pairs) + pairs * sizeof(int4); }
@@ -1016,17 +689,27 @@ dsa_status_t launch_dense(const DenseParams& p, const void* q, const void* kv, i
   cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_kernel<F8>, p, qmap, kvmap, ropemap, rowmap);
   if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_kernel launch failed: %s", cudaGetErrorString(e));
-  if (p.cut) {
-    if ((st = allow_smem(dense_mla_merge_kernel, 0, g_smem_dense_merge)) != DSA_OK) return st;
-    cfg.gridDim = dim3(32, static_cast<unsigned>(pairs));
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, dense_mla_merge_kernel, p);
-    if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_merge_kernel launch failed: %s", cudaGetErrorString(e));
-  }
-  return check_launch("dense_mla_kernel");
+  return DSA_OK;
 }
+
+template <bool QUAD>
+dsa_status_t launch_merge(const DenseParams& p, int runs, cudaStream_t s) {
+  dsa_status_t st = allow_smem(dense_mla_merge_kernel<QUAD>, 0, g_smem_merge[QUAD]);
+  if (st != DSA_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(QUAD ? 64 : 32, static_cast<unsigned>(runs));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_merge_kernel<QUAD>, p);
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_merge_kernel launch failed: %s", cudaGetErrorString(e));
+  return DSA_OK;
+}
+
 
 dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_stride, int32_t num_blocks,
                         const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
@@ -1094,7 +777,19 @@ dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_st
     d.desc = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(d.ml_part) + ml_part_bytes(pairs));
   }
   d.dev_status = dev_status;
-  return f8 ? launch_dense<true>(d, q, kv_cache, pairs, s) : launch_dense<false>(d, q, kv_cache, pairs, s);
+  // Requests of two row tiles and more on average go to clusters of four CTAs,
+  // which take 256 rows at a time. Not when row tiles may not be cut: then a
+  // token's result must not depend on how long the other requests are.
+  const int quads = d.cut && static_cast<int64_t>(T) * H >= int64_t(256) * B ? num_quads(f8) : 0;
+  if (quads > 0) {
+    d.tpt = 256 / H;
+    st = launch_quads(d, f8, q, kv_cache, quads, s);
+    if (st == DSA_OK) st = launch_merge<true>(d, quads, s);
+  } else {
+    st = f8 ? launch_dense<true>(d, q, kv_cache, pairs, s) : launch_dense<false>(d, q, kv_cache, pairs, s);
+    if (st == DSA_OK && d.cut) st = launch_merge<false>(d, pairs, s);
+  }
+  return st == DSA_OK ? check_launch(name) : st;
 }
 
 }  // namespace

@@ -1,0 +1,365 @@
+// Shared by the dense MLA attention kernels: a batch as work (row tiles and
+// steps of 128 keys, cut into runs), its block table, and the loads of keys.
+//
+// Rows: the (token, head) rows of a request, whole tokens at a time, form row
+// tiles of at most 128 rows (256 in the four-CTA kernel); all rows of a request
+// see the same latent rows. The steps of all row tiles form one sequence, cut
+// into equal runs, one per group of CTAs (one persistent wave). A row tile cut
+// by a run's end leaves fp32 partials, at most two per run.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace dense {
+
+using namespace ptx;
+
+constexpr int kDk = 576, kDv = 512, kF8Row = 656;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kTile = 128;    // keys of a step
+constexpr int kSlot = 16384;  // 64 keys x 128 dims
+constexpr float kRescaleThreshold = 8.f;  // log2 units
+constexpr long long kWaitLimitCycles = 2000000000ll;
+constexpr int kMinRun = 4;  // steps a run has at least when row tiles may be cut
+
+struct DenseParams {
+  int32_t num_blocks, rows_per_block, total_rows;
+  const int32_t* block_table;
+  int32_t bt_stride;
+  const int32_t *seq_lens, *qsl;
+  int32_t B, T, H, tpt;      // tpt: tokens per row tile
+  int32_t block_size, bs64;  // bs64 = block_size / 64
+  float scale_log2;
+  const uint8_t* kv;  // the fp8 cache
+  int32_t cut;    // row tiles may be cut
+  int32_t out32;  // out is 32-byte aligned
+  uint16_t* out;
+  float* lse;
+  // Partials, two per run: slot 2 n is the row tile that run n goes on with
+  // from the run before, 2 n + 1 the one it leaves to the next
+  float4* o_part;   // [slot][row halves][groups of 4 TMEM columns][128 lanes]
+  float2* ml_part;  // [slot][rows of a row tile]: max (log2 units), sum
+  int4* desc;       // per run: the cut row tile that starts in it (first row, rows, further parts)
+  int32_t* dev_status;
+};
+
+// The run of a group of CTAs: its first request, row tile and step, and its
+// steps [pos, end) of all; per: steps of every run.
+struct Run {
+  int32_t b, tile, k0, pad;
+  int64_t pos, end, per;
+};
+
+// A request's rows as work: row tile i has steps(i) = max(1, ceil(keys its
+// last token sees / 128)).
+struct Request {
+  int32_t q0, q_len, n_tiles, kv_len;  // kv_len: its cached keys that the table can hold
+  int32_t c;     // position of its first new token (a length below 0 counts as 0)
+  bool uneven;   // lengths that contradict each other: every tile is charged kv_len
+};
+
+__device__ __forceinline__ Request load_request(const DenseParams& p, int b) {
+  Request r;
+  const int q0 = min(max(__ldg(p.qsl + b), 0), p.T), q1 = min(max(__ldg(p.qsl + b + 1), 0), p.T);
+  const int64_t sl = __ldg(p.seq_lens + b), cap = static_cast<int64_t>(p.bt_stride) * p.block_size;
+  r.q0 = q0;
+  r.q_len = max(q1 - q0, 0);
+  r.n_tiles = (r.q_len + p.tpt - 1) / p.tpt;
+  // at most 2^31 - 256, so that sums of a few steps stay within 31 bits
+  r.kv_len = static_cast<int32_t>(max(int64_t(0), min(min(sl, cap), int64_t(0x7FFFFF00))));
+  r.c = static_cast<int32_t>(max(sl, int64_t(0))) - r.q_len;
+  r.uneven = r.c < 0 || r.kv_len != sl;
+  return r;
+}
+// keys visible to the token i (from 0) of the request
+__device__ __forceinline__ int visible(const Request& r, int i) {
+  return max(0, min(r.c + i + 1, r.kv_len));
+}
+__device__ __forceinline__ int steps_of(const DenseParams& p, const Request& r, int tile) {
+  const int keys = r.uneven ? r.kv_len : visible(r, min(r.q_len, (tile + 1) * p.tpt) - 1);
+  return max(1, (keys + kTile - 1) / kTile);
+}
+// sum over i < n of floor((a i + b) / 128)
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
+  if ((a & (a - 1)) == 0) {  // a divides 128: floor((i + b / a) / (128 / a)), a whole run of each quotient
+    const int sh = 7 - (31 - __clz(static_cast<int>(a)));
+    const auto upto = [&](int64_t x) {  // sum over j < x of floor(j / 2^sh)
+      const int64_t k = x >> sh;
+      return ((k * (k - 1) / 2) << sh) + k * (x & ((int64_t(1) << sh) - 1));
+    };
+    const int64_t b0 = b / a;
+    return upto(n + b0) - upto(b0);
+  }
+  // the lattice points under the line, by the Euclidean algorithm
+  int64_t sum = 0, m = 128;
+  while (true) {
+    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const int64_t top = a * n + b;
+    if (top < m) return sum;
+    n = top / m;
+    b = top % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+}
+// steps of the request's row tiles before tile n
+__device__ __forceinline__ int64_t steps_before(const DenseParams& p, const Request& r, int n) {
+  if (r.uneven) return static_cast<int64_t>(n) * steps_of(p, r, 0);
+  if (n == 0) return 0;
+  if (n < r.n_tiles) return floor_sum(n, p.tpt, static_cast<int64_t>(r.c) + p.tpt + kTile - 1);
+  return floor_sum(n - 1, p.tpt, static_cast<int64_t>(r.c) + p.tpt + kTile - 1) + steps_of(p, r, n - 1);
+}
+
+// A run of steps, segment by segment (a segment: the steps of one row tile).
+struct Cursor {
+  Request req;
+  int32_t b, tile, nk, k0, k1;
+  int32_t left;  // steps of the run from this segment on
+  __device__ __forceinline__ void cut(const DenseParams& p) {
+    nk = steps_of(p, req, tile);
+    k1 = p.cut ? min(nk, k0 + left) : nk;
+  }
+  __device__ __forceinline__ bool start(const DenseParams& p, const Run* s) {
+    b = s->b;
+    tile = s->tile;
+    k0 = k1 = nk = s->k0;
+    left = static_cast<int32_t>(s->end - s->pos);
+    if (left <= 0) return false;
+    req = load_request(p, b);
+    cut(p);
+    return true;
+  }
+  __device__ __forceinline__ bool next(const DenseParams& p) {
+    left -= k1 - k0;
+    if (left <= 0) return false;
+    k0 = 0;
+    if (++tile >= req.n_tiles) {
+      tile = 0;
+      do {
+        if (++b >= p.B) return false;
+        req = load_request(p, b);
+      } while (req.n_tiles == 0);
+    }
+    cut(p);
+    return true;
+  }
+};
+
+// The cache rows of a unit of 64 keys: their first row (total_rows, which
+// reads as zeros, where there is none) and how many of them exist.
+struct Rows {
+  int32_t row, n;
+};
+// A warp's view of a row tile's part of the block table: lane l holds the
+// entry of unit base + l, and the entries of the 32 units behind are in flight,
+// so that no step waits for the table. Called by whole warps.
+struct Units {
+  int32_t base, row, ahead;
+  __device__ __forceinline__ int32_t entry(const DenseParams& p, const Cursor& c, int unit) const {
+    const int64_t key = static_cast<int64_t>(unit) * 64;
+    return key < c.req.kv_len ? __ldg(p.block_table + static_cast<int64_t>(c.b) * p.bt_stride + unit / p.bs64) : 0;
+  }
+  __device__ __forceinline__ int32_t first_row(const DenseParams& p, const Cursor& c, int32_t blk, int unit, bool rep) const {
+    if (blk < 0 || blk >= p.num_blocks) {
+      if (rep && static_cast<int64_t>(unit) * 64 < c.req.kv_len) report(p.dev_status, DSA_DEVERR_BLOCK_OOB);
+      return -1;
+    }
+    return blk * p.rows_per_block + (unit % p.bs64) * 64;
+  }
+  __device__ __forceinline__ void start(const DenseParams& p, const Cursor& c, int lane, bool rep) {
+    base = 2 * c.k0;
+    row = entry(p, c, base + lane);
+    ahead = entry(p, c, base + 32 + lane);
+    row = first_row(p, c, row, base + lane, rep);
+  }
+  // units are asked for in ascending order, at most 32 behind the last
+  __device__ __forceinline__ Rows get(const DenseParams& p, const Cursor& c, int unit, int lane, bool rep) {
+    if (unit >= base + 32) {
+      base += 32;
+      row = first_row(p, c, ahead, base + lane, rep);
+      ahead = entry(p, c, base + 32 + lane);
+    }
+    const int left = c.req.kv_len - unit * 64;
+    const int32_t first = __shfl_sync(0xFFFFFFFFu, row, (unit - base) & 31);
+    if (left <= 0 || first < 0) return {p.total_rows, 0};
+    return {first, min(left, 64)};
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// mbar_wait with one answer for the warp
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+}
+
+// Loads 64 keys x 64 * blocks dims (dim block d0 on) by the whole warp. The
+// rows behind a request's last key are not its own and may hold anything,
+// NaN included, so they are gathered from past the cache's end, as zeros.
+__device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* box, const CUtensorMap* row_map,
+                                          uint32_t bar, Rows x, int32_t total_rows, int d0, int blocks, int lane) {
+  if (x.n == 0 || x.n == 64) {
+    if (lane == 0) tma_load_3d_pair(dst, box, bar, 0, x.row, d0);
+  } else {
+    const int g = lane & 15, d = lane >> 4;
+    if (d < blocks) {
+      int r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = 4 * g + i < x.n ? x.row + 4 * g + i : total_rows;
+      tma_gather4_pair(dst + d * 8192 + g * 512, row_map, bar, (d0 + d) * 64, r[0], r[1], r[2], r[3]);
+    }
+  }
+  __syncwarp();
+}
+
+// ---- fp8 cache: a row's 128 codes of one group are 8 lanes' 16 bytes, read
+// straight into registers, decoded (code * scale in fp32, rounded to bf16:
+// the tensor cores take bf16) and stored as the swizzled tile the copies of
+// the bf16 cache would bring.
+__device__ __forceinline__ float2 mul2(float2 a, float s) {  // two products in one instruction
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmul.rn.f32x2 c, a, b;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(s));
+  return r;
+}
+__device__ __forceinline__ uint32_t decode2(uint32_t two, float sc) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  const float2 v = mul2(f, sc);
+  return pack_bf16(v.x, v.y);
+}
+__device__ __forceinline__ uint4 decode8(uint32_t a, uint32_t b, float sc) {
+  return make_uint4(decode2(a, sc), decode2(a >> 16, sc), decode2(b, sc), decode2(b >> 16, sc));
+}
+struct Codes {
+  uint4 c;
+  float sc;
+};
+// 16 codes of a key's group (lane8: which), none where the key does not exist.
+// The upper four lanes of a key write another 64-dim block than the lower
+// four, in the same banks: they hold and store their two 16-byte chunks in the
+// other order.
+__device__ __forceinline__ Codes fetch16(const uint8_t* row, int group, int lane8, bool exists) {
+  Codes v{make_uint4(0u, 0u, 0u, 0u), 0.f};
+  if (exists) {
+    // volatile: issued here, ahead of the waits, not where the values are used
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.c.x), "=r"(v.c.y), "=r"(v.c.z), "=r"(v.c.w)
+                 : "l"(row + 128 * group + 16 * lane8));
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v.sc) : "l"(row + kDv + 4 * group));
+  }
+  return v;
+}
+struct Decoded {
+  uint4 first, second;
+};
+__device__ __forceinline__ Decoded decode16(const Codes& v, bool swap) {
+  return {decode8(swap ? v.c.z : v.c.x, swap ? v.c.w : v.c.y, v.sc),
+          decode8(swap ? v.c.x : v.c.z, swap ? v.c.y : v.c.w, v.sc)};
+}
+
+// Run `index` of n_runs: every CTA sums the requests' steps itself. `scratch`
+// is shared memory that nothing else uses yet.
+template <int kThreads>
+__device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* scratch, int index, int n_runs) {
+  int64_t* sums = reinterpret_cast<int64_t*>(scratch);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kThreads / 32;
+  const bool once = p.B <= kThreads;
+  int64_t w = 0, incl = 0;
+  Request r = {};
+  const auto scan = [&](int b) {  // steps of request b, and their inclusive sum over the block's requests
+    w = 0;
+    if (b < p.B) {
+      r = load_request(p, b);
+      if (r.uneven && r.q_len > 0 && index == 0) {
+        report(p.dev_status, DSA_DEVERR_SEQ_LEN);
+      }
+      w = steps_before(p, r, r.n_tiles);
+    }
+    incl = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+      if (lane >= off) incl += u;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int64_t all = 0;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) incl += sums[i];
+      all += sums[i];
+    }
+    return all;
+  };
+  int64_t total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) total += scan(b0 + tid);
+  int64_t per = (total + n_runs - 1) / n_runs;
+  if (p.cut) per = max(per, int64_t(kMinRun));
+  const int64_t u0 = per * index, u1 = min(u0 + per, total);
+  if (tid == 0) {
+    s->per = per;
+    s->pos = s->end = 0;
+  }
+  __syncthreads();
+  if (u0 < u1) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int64_t all = once ? total : scan(b0 + tid);
+      const int64_t from = base + incl - w;
+      if (w > 0 && from <= u0 && u0 < from + w) {
+        const int64_t u = u0 - from;
+        int lo = 0, hi = r.n_tiles - 1;  // the last row tile that starts at or before u
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (steps_before(p, r, mid) <= u) lo = mid; else hi = mid - 1;
+        }
+        const int64_t at = steps_before(p, r, lo);
+        s->b = b0 + tid;
+        s->tile = lo;
+        s->k0 = static_cast<int32_t>(u - at);
+        s->pos = u0;
+        s->end = u1;
+        if (!p.cut && u > at) {  // the row tile belongs to the run it starts in: begin with the next
+          s->k0 = 0;
+          s->pos = from + steps_before(p, r, lo + 1);
+          if (lo + 1 < r.n_tiles) {
+            s->tile = lo + 1;
+          } else if (s->pos < u1) {
+            int b = b0 + tid;
+            do ++b; while (load_request(p, b).n_tiles == 0);
+            s->b = b;
+            s->tile = 0;
+          }
+        }
+      }
+      base += all;
+    }
+  }
+  fence_proxy_async_smem();  // the copies that follow write where the scratch was
+  __syncthreads();
+}
+
+// Number of 4-CTA clusters the current device runs at once, 0 when it cannot.
+int num_quads(bool f8);
+// Enqueues the four-CTA kernel (p.tpt tokens per row tile of 256 rows).
+dsa_status_t launch_quads(const DenseParams& p, bool f8, const void* q, const void* kv, int quads, cudaStream_t s);
+
+}  // namespace dense
+}  // namespace dsa

@@ -1,0 +1,666 @@
+// Dense causal MLA attention for requests of several row tiles (chunks of a
+// prompt, multi-token steps): row tiles of 256 rows on clusters of four CTAs.
+//
+// The pair kernel's M = 128 MMAs fill half of the tensor cores' rate; M = 256
+// fills it, but 256 rows x 512 dims of fp32 output take the whole tensor
+// memory of two CTAs. So two more CTAs make the scores:
+//   CTAs 0, 1   S = Q K^T for rows [128 a, 128 a + 128), M = 256, N = 128: q's
+//               latent dims in tensor memory (256 columns), its rope dims in
+//               shared memory, each CTA bringing 64 of the step's 128 keys;
+//               softmax; P (bf16) goes to CTA 2 + a through distributed shared
+//               memory, with the factor by which the row's output shrinks;
+//   CTAs 2, 3   O += P V, M = 256, N = 2 x 256: CTA 2 + a holds the outputs of
+//               rows [128 a, 128 a + 128) in all 512 columns and brings value
+//               dims [256 a, 256 a + 256) of all 128 keys.
+// Per step an SM takes in 72 KB of keys (CTAs 0, 1), or 64 KB of values and 32
+// KB of P (CTAs 2, 3): ~3070 clocks at the ~32 bytes per clock that an SM
+// takes in, against 2300 and 2050 of MMA, for twice the rows of a pair's step.
+#include <algorithm>
+
+#include "dense_mla.cuh"
+
+namespace dsa {
+namespace dense {
+namespace {
+
+constexpr int kWorkers = 8;  // warps 0-7: softmax (CTAs 0, 1), rescaling and results (CTAs 2, 3)
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kThreads = 320;
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColQ = 256;  // CTAs 0, 1: S 2 x 128, q 256; CTAs 2, 3: O 512
+
+// Shared memory. CTAs 0, 1: a ring of 13 slots of 16 KB (q's 8 latent blocks of
+// 128 rows x 64 dims when a row tile begins, then per step 4 slots of 64 keys
+// x 128 dims and one of 64 keys x 64 rope dims), q's rope block, row maxima.
+// CTAs 2, 3: a ring of 10 slots (per step 4 of 64 keys x 128 dims), P as two
+// buffers of 2 blocks of 128 rows x 64 keys, factors, (max, sum).
+constexpr int kRingS = 13, kRingV = 10;
+constexpr int kSmRopeQ = kRingS * kSlot, kSmRed = kSmRopeQ + 16384;
+constexpr int kSmP = kRingV * kSlot, kSmAlpha = kSmP + 2 * 32768, kSmMl = kSmAlpha + 2 * 128 * 4;
+constexpr int kSmBar = kSmRed + 2048, kSmTotal = kSmBar + 1024;
+static_assert(kSmTotal <= 232448 && kSmMl + 1024 <= kSmBar, "shared memory");
+
+struct Bars {  // at the same offset in every CTA
+  uint64_t full[kRingS], empty[kRingS];  // ring slots; full: of both CTAs of a pair, the even one's barrier
+  // CTAs 0, 1
+  uint64_t q_full, q_copied;  // q landed in the ring; copied to tensor memory by this CTA's warps
+  uint64_t q_ready;           // ... by both CTAs' (CTA 0's barrier)
+  uint64_t rope_free;         // the row tile's last S has read q's rope block
+  uint64_t s_full[2], s_free[2];  // S complete; S read by both CTAs' warps (CTA 0's barrier)
+  uint64_t rows[4];           // the two warps that share 32 rows
+  uint64_t ml_free;           // CTA 2 + a has read the row tile's (max, sum)
+  // CTAs 2, 3
+  uint64_t p_full[2], p_ready[2];  // P landed; P fenced and O rescaled in both CTAs (CTA 2's barrier)
+  uint64_t ml_full;
+  // all: O += P V of a step complete, i.e. the P buffer is free
+  uint64_t pv_done[2];
+  uint32_t tmem;
+  volatile int abort;
+  Run run;
+};
+static_assert(sizeof(Bars) <= 1024, "barrier block too large");
+
+__device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t ctas) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(ctas)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc_lo, uint32_t bdesc_hi,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(bdesc_lo), "r"(bdesc_hi), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void st_async_b32(uint32_t cluster_addr, uint32_t cluster_bar, uint32_t a) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr), "r"(a),
+               "r"(cluster_bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_async_v2(uint32_t cluster_addr, uint32_t cluster_bar, uint32_t a, uint32_t b) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(cluster_addr),
+               "r"(a), "r"(b), "r"(cluster_bar)
+               : "memory");
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity));
+}
+
+// A ring position that walks its slots; every slot's empty barrier changes
+// phase once per turn (full too, but for slots that held q).
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      ++turn;
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __grid_constant__ DenseParams p,
+                                                                     const __grid_constant__ CUtensorMap qmap,
+                                                                     const __grid_constant__ CUtensorMap kvmap,
+                                                                     const __grid_constant__ CUtensorMap ropemap,
+                                                                     const __grid_constant__ CUtensorMap rowmap) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars* s = reinterpret_cast<Bars*>(smem + kSmBar);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_ctarank()), a = rank & 1;  // a: row half
+  const bool values = rank >= 2;
+  const int quad = blockIdx.x >> 2, n_quads = gridDim.x >> 2;
+
+  if (smem_u32(smem) & 1023u) {  // the tiles need it (without static arrays the dynamic part starts there)
+    if (tid == 0) report(p.dev_status, DSA_DEVERR_TIMEOUT);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kRingS; ++i) {
+      mbar_init(&s->full[i], 1);
+      mbar_init(&s->empty[i], 1);
+    }
+    mbar_init(&s->q_full, 1);
+    mbar_init(&s->q_copied, kWorkers);
+    mbar_init(&s->q_ready, 2 * kWorkers);
+    mbar_init(&s->rope_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s->s_full[i], 1);
+      mbar_init(&s->s_free[i], 2 * kWorkers);
+      mbar_init(&s->p_full[i], 1);
+      mbar_init(&s->p_ready[i], 2 * kWorkers);
+      mbar_init(&s->pv_done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&s->rows[i], 2);
+    mbar_init(&s->ml_free, kWorkers);
+    mbar_init(&s->ml_full, 1);
+    fence_mbar_init();
+    s->abort = 0;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc_pair(&s->tmem, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (tid == kLoadWarp * 32) {
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kvmap);
+    prefetch_tmap(&ropemap);
+    prefetch_tmap(&rowmap);
+  }
+  tc_fence_before();
+  cluster_sync_all();  // all CTAs' barriers exist
+  tc_fence_after();
+  const uint32_t tmem = s->tmem;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  plan_run<kThreads>(p, &s->run, smem, quad, n_quads);
+
+  const auto abort_now = [&] {
+    s->abort = 1;
+    report(p.dev_status, DSA_DEVERR_TIMEOUT);
+  };
+  // a barrier's or buffer's address in another CTA
+  const auto in_cta = [&](const void* x, int cta) { return mapa_shared(smem_u32(x), static_cast<uint32_t>(cta)); };
+  const int even = rank & ~1;
+  Cursor c;
+
+  if (warp == kLoadWarp && !values) {
+    // ---------------- q of each row tile, then the own keys of its steps
+    Ring<kRingS> ring;
+    bool ok = true;
+    int seg = 0;
+    const auto claim = [&] {  // the slot's former content has been used
+      if (ring.turn > 0 && !warp_wait(&s->empty[ring.slot], (ring.turn - 1) & 1)) {
+        if (lane == 0) abort_now();
+        ok = false;
+      }
+      return ok;
+    };
+    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
+      const int row0 = (c.req.q0 + c.tile * p.tpt) * p.H + 128 * a;
+      if (seg > 0 && !warp_wait(&s->rope_free, (seg - 1) & 1)) {
+        if (lane == 0) abort_now();
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&s->q_full, 9 * 16384);
+        tma_load_3d_pair(smem_u32(smem + kSmRopeQ), &qmap, in_cta(&s->q_full, rank), 0, row0, 8);
+      }
+      __syncwarp();
+      for (int i = 0; i < 8 && claim(); ++i, ring.next()) {
+        if (lane == 0)
+          tma_load_3d_pair(smem_u32(smem + ring.slot * kSlot), &qmap, in_cta(&s->q_full, rank), 0, row0, i);
+        __syncwarp();
+      }
+      Units u;
+      u.start(p, c, lane, true);
+      for (int kt = c.k0; kt < c.k1 && ok; ++kt) {
+        const Rows x = u.get(p, c, 2 * kt + a, lane, true);
+        for (int k = 0; k < 5 && claim(); ++k, ring.next()) {
+          if (a == 0 && lane == 0) mbar_arrive_expect_tx(&s->full[ring.slot], k < 4 ? 2 * kSlot : kSlot);
+          const uint32_t dst = smem_u32(smem + ring.slot * kSlot), bar = in_cta(&s->full[ring.slot], even);
+          if (k < 4) load_keys(dst, &kvmap, &rowmap, bar, x, p.total_rows, 2 * k, 2, lane);
+          else load_keys(dst, &ropemap, &rowmap, bar, x, p.total_rows, 8, 1, lane);
+        }
+      }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else if (warp == kLoadWarp) {
+    // ---------------- all keys of each step, the own value dims
+    Ring<kRingV> ring;
+    bool ok = true;
+    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p)) {
+      Units u;
+      u.start(p, c, lane, false);
+      for (int kt = c.k0; kt < c.k1 && ok; ++kt) {
+        const Rows x0 = u.get(p, c, 2 * kt, lane, false), x1 = u.get(p, c, 2 * kt + 1, lane, false);
+        for (int k = 0; k < 4; ++k, ring.next()) {
+          if (ring.turn > 0 && !warp_wait(&s->empty[ring.slot], (ring.turn - 1) & 1)) {
+            if (lane == 0) abort_now();
+            ok = false;
+            break;
+          }
+          if (a == 0 && lane == 0) mbar_arrive_expect_tx(&s->full[ring.slot], 2 * kSlot);
+          load_keys(smem_u32(smem + ring.slot * kSlot), &kvmap, &rowmap, in_cta(&s->full[ring.slot], even),
+                    k < 2 ? x0 : x1, p.total_rows, 2 * (2 * a + (k & 1)), 2, lane);
+        }
+      }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else if (warp == kMmaWarp && !values) {
+    // ---------------- S, issued by CTA 0 for both. The warp stays converged,
+    // so that the descriptors live in uniform registers; one lane issues
+    if (rank == 0) {
+      const uint32_t idesc = idesc_bf16(256, kTile, false, false);
+      const uint64_t dk = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
+      Ring<kRingS> ring;
+      uint32_t phases = 0;  // of the slots' full barriers: q's uses of a slot do not count there
+      bool ok = true;
+      int it = 0, seg = 0;
+      for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
+        for (int i = 0; i < 8; ++i) ring.next();
+        ok = warp_wait(&s->q_ready, seg & 1);
+        for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
+          const int buf = it & 1;
+          if (it >= 2) ok = warp_wait(&s->s_free[buf], ((it >> 1) - 1) & 1);
+          const uint32_t d = tmem + kColS + 128 * buf;
+#pragma unroll 1
+          for (int k = 0; k < 5 && ok; ++k, ring.next()) {
+            ok = warp_wait(&s->full[ring.slot], (phases >> ring.slot) & 1);
+            if (!ok) break;
+            phases ^= 1u << ring.slot;
+            tc_fence_after();
+            const uint32_t b0 = k_lo + ((ring.slot * kSlot) >> 4);
+            if (k < 4) {
+              const uint32_t q0 = tmem + kColQ + k * 64, acc0 = k > 0 ? 1u : 0u;
+              if (elect_one()) {
+#pragma unroll
+                for (int st = 0; st < 8; ++st)
+                  mma_bf16_ts_pair(d, q0 + st * 8, b0 + (((st >> 2) * 8192 + (st & 3) * 32) >> 4), k_hi, idesc,
+                                   st > 0 ? 1u : acc0);
+                commit_to(&s->empty[ring.slot], 0x3);
+              }
+            } else {
+              const bool last = kt + 1 == c.k1;
+              if (elect_one()) {
+#pragma unroll
+                for (int st = 0; st < 4; ++st)
+                  mma_bf16_ss_pair(d, k_lo + ((kSmRopeQ + st * 32) >> 4), k_hi, b0 + ((st * 32) >> 4), k_hi, idesc, 1u);
+                commit_to(&s->empty[ring.slot], 0x3);
+                commit_to(&s->s_full[buf], 0x3);
+                if (last) commit_to(&s->rope_free, 0x3);
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (!ok && lane == 0) abort_now();
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ---------------- O += P V, issued by CTA 2 for both
+    if (rank == 2) {
+      const uint32_t idesc = idesc_bf16(256, 256, false, true);
+      // P: 8-row groups 1024 bytes apart; values (dims along N): 64-dim blocks 8192 bytes apart
+      const uint64_t dp = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      const uint64_t dv = smem_desc(smem_u32(smem), 8192, 1024, kSwizzle128B);
+      const uint32_t p_lo = static_cast<uint32_t>(dp), p_hi = static_cast<uint32_t>(dp >> 32);
+      const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
+      Ring<kRingV> ring;
+      bool ok = true;
+      int it = 0;
+      for (bool more = c.start(p, &s->run); more && ok; more = c.next(p)) {
+        for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
+          const int buf = it & 1;
+          ok = warp_wait(&s->p_ready[buf], (it >> 1) & 1);
+#pragma unroll 1
+          for (int kh = 0; kh < 2 && ok; ++kh) {  // 64 keys each: a slot of 128 dims after the other
+            const int s0 = ring.slot;
+            ok = warp_wait(&s->full[ring.slot], ring.turn & 1);
+            ring.next();
+            const int s1 = ring.slot;
+            ok = ok && warp_wait(&s->full[ring.slot], ring.turn & 1);
+            ring.next();
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a0 = p_lo + ((kSmP + buf * 32768 + kh * 16384) >> 4);
+            const uint32_t b0 = v_lo + ((s0 * kSlot) >> 4), b1 = v_lo + ((s1 * kSlot) >> 4);
+            const uint32_t acc0 = (kt > c.k0 || kh > 0) ? 1u : 0u;
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) {  // 16 keys each
+                mma_bf16_ss_pair(tmem, a0 + ((ks * 32) >> 4), p_hi, b0 + ((ks * 2048) >> 4), v_hi, idesc, ks > 0 ? 1u : acc0);
+                mma_bf16_ss_pair(tmem + 256, a0 + ((ks * 32) >> 4), p_hi, b1 + ((ks * 2048) >> 4), v_hi, idesc,
+                                 ks > 0 ? 1u : acc0);
+              }
+              commit_to(&s->empty[s0], 0xC);
+              commit_to(&s->empty[s1], 0xC);
+              if (kh == 1) commit_to(&s->pv_done[buf], 0xF);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (!ok && lane == 0) abort_now();
+    }
+    __syncwarp();
+  } else if (!values) {
+    // ---------------- softmax: TMEM lane = row; the two warps of a lane group
+    // take 64 keys each
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float* red = reinterpret_cast<float*>(smem + kSmRed);  // [step parity][half][row]
+    const uint32_t q_ready = in_cta(&s->q_ready, 0), s_free = in_cta(&s->s_free[0], 0);
+    const uint32_t p_dst = in_cta(smem + kSmP, 2 + a) + half * 16384, p_full = in_cta(&s->p_full[0], 2 + a);
+    const uint32_t alpha_dst = in_cta(smem + kSmAlpha, 2 + a) + row * 4;
+    Ring<kRingS> ring;
+    bool ok = true;
+    int it = 0, seg = 0;
+    uint32_t meets = 0;
+    const auto meet = [&] {  // the two warps that hold the same rows: what each wrote is seen by both
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s->rows[warp & 3]);
+      return warp_wait(&s->rows[warp & 3], meets++ & 1);
+    };
+    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
+      // q's latent dims -> tensor memory (the A operand); its slots are then free
+      if (!warp_wait(&s->q_full, seg & 1)) {
+        if (lane == 0) abort_now();
+        break;
+      }
+      for (int i = 0; i < 8; ++i, ring.next()) {
+        if ((i & 1) != half) continue;
+        const uint8_t* blk = smem + ring.slot * kSlot;
+        uint32_t v[32];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint4 w = *reinterpret_cast<const uint4*>(blk + sw128_offset(row, k));
+          v[4 * k] = w.x;
+          v[4 * k + 1] = w.y;
+          v[4 * k + 2] = w.z;
+          v[4 * k + 3] = w.w;
+        }
+        tmem_st32(lane_base + kColQ + 32 * i, v);
+      }
+      tmem_st_wait();
+      fence_proxy_async_smem();  // the slots are refilled by TMA
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&s->q_copied);
+        mbar_arrive_remote_relaxed(q_ready);
+      }
+      if (warp == 0) {
+        if (!warp_wait(&s->q_copied, seg & 1)) {
+          if (lane == 0) abort_now();
+          break;
+        }
+        if (lane < 8) mbar_arrive(&s->empty[(ring.slot + kRingS - 8 + lane) % kRingS]);
+        __syncwarp();
+      }
+      for (int i = 0; i < 5 * (c.k1 - c.k0) % (kRingS); ++i) {
+        if (++ring.slot == kRingS) ring.slot = 0;
+      }
+
+      const int in_tile = 128 * a + row;
+      const int tok = c.tile * p.tpt + in_tile / p.H;
+      const bool live = in_tile < p.tpt * p.H && tok < c.req.q_len;
+      const int lim = live ? visible(c.req, tok) : 0;
+      float m = kNegSentinel, l = 0.f;
+      Units u;
+      u.start(p, c, lane, false);
+      for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
+        const int buf = it & 1;
+        const Rows x = u.get(p, c, 2 * kt + half, lane, false);
+        const int n = x.n == 0 ? 0 : lim - kt * kTile - half * 64;  // of this thread's 64 keys, visible ones
+        if (!warp_wait(&s->s_full[buf], (it >> 1) & 1)) {
+          if (lane == 0) abort_now();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float sc[64];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+          tmem_ld32_sync(lane_base + kColS + 128 * buf + 64 * half + 32 * h, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sc[32 * h + i] = __uint_as_float(v[i]) * p.scale_log2;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(s_free + 8 * buf);
+        if (n < 64) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) sc[i] = i < n ? sc[i] : -INFINITY;
+        }
+        float mt = sc[0];
+#pragma unroll
+        for (int i = 1; i < 64; ++i) mt = fmaxf(mt, sc[i]);
+        float* rd = red + buf * 256;
+        rd[half * 128 + row] = mt;
+        if (!meet()) {
+          if (lane == 0) abort_now();
+          ok = false;
+          break;
+        }
+        mt = fmaxf(rd[row], rd[128 + row]);
+        const bool rescale = mt > m + kRescaleThreshold;
+        const float m_new = rescale ? mt : m, neg_m = -m_new;
+        const float alpha = rescale ? ex2_approx(m - m_new) : 1.f;
+        m = m_new;
+        // P's buffer is free once PV of the step before the last is done
+        if (it >= 2 && !warp_wait(&s->pv_done[buf], ((it >> 1) - 1) & 1)) {
+          if (lane == 0) abort_now();
+          ok = false;
+          break;
+        }
+        const uint32_t bar = p_full + 8 * buf, dst = p_dst + buf * 32768;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // the sum takes the fp32 weights; the product takes them rounded to bf16
+            const float e0 = ex2_approx(sc[8 * k + 2 * i] + neg_m), e1 = ex2_approx(sc[8 * k + 2 * i + 1] + neg_m);
+            s0 += e0;
+            s1 += e1;
+            pk[i] = pack_bf16(e0, e1);
+          }
+          st_async_v4(dst + sw128_offset(row, k), bar, pk[0], pk[1], pk[2], pk[3]);
+        }
+        if (half == 0) st_async_b32(alpha_dst + buf * 512, bar, __float_as_uint(alpha));
+        l = l * alpha + (s0 + s1);
+      }
+      if (!ok) break;
+      // the row tile's (or its part's) maximum and sum
+      float* sums = red + (it & 1) * 256;  // the maxima of the step before the last: read by both
+      sums[half * 128 + row] = l;
+      ok = meet();
+      l = sums[row] + sums[128 + row];
+      ok = ok && meet();
+      if (ok && seg > 0 && half == 0) ok = warp_wait(&s->ml_free, (seg - 1) & 1);
+      if (!ok) {
+        if (lane == 0) abort_now();
+        break;
+      }
+      if (half == 0)
+        st_async_v2(in_cta(smem + kSmMl, 2 + a) + row * 8, in_cta(&s->ml_full, 2 + a), __float_as_uint(m), __float_as_uint(l));
+    }
+  } else {
+    // ---------------- O: rescaling when a row's maximum has grown, and the
+    // results; TMEM lane = row, the two warps of a lane group take 256 columns each
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    const uint32_t o_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * half;
+    const float* alphas = reinterpret_cast<const float*>(smem + kSmAlpha);
+    const float2* mls = reinterpret_cast<const float2*>(smem + kSmMl);
+    const uint32_t p_ready = in_cta(&s->p_ready[0], 2), ml_free = in_cta(&s->ml_free, a);
+    bool ok = true;
+    int it = 0, seg = 0;
+    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
+      for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
+        const int buf = it & 1;
+        if (tid == 0) mbar_arrive_expect_tx(&s->p_full[buf], 32768 + 512);
+        __syncwarp();
+        ok = warp_wait_cluster(&s->p_full[buf], (it >> 1) & 1);
+        const float alpha = ok ? alphas[buf * 128 + row] : 1.f;
+        if (ok && kt > c.k0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+          ok = warp_wait(&s->pv_done[buf ^ 1], ((it - 1) >> 1) & 1);
+          if (ok) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < 256; q += 32) {
+              uint32_t o[32];
+              tmem_ld32_sync(o_base + q, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(o_base + q, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        if (!ok) {
+          if (lane == 0) abort_now();
+          break;
+        }
+        // the stores of the other CTA are seen here; the tensor cores read
+        // them through the async proxy
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(p_ready + 8 * buf);
+      }
+      if (!ok) break;
+      if (tid == 0) mbar_arrive_expect_tx(&s->ml_full, 128 * 8);
+      __syncwarp();
+      ok = warp_wait_cluster(&s->ml_full, seg & 1);
+      const float2 ml = ok ? mls[row] : make_float2(0.f, 0.f);
+      ok = ok && warp_wait(&s->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+      if (!ok) {
+        if (lane == 0) abort_now();
+        break;
+      }
+      // the value is consumed before the arrival lets it be overwritten
+      asm volatile("" ::"f"(ml.x), "f"(ml.y) : "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_relaxed(ml_free);
+      tc_fence_after();
+      const int in_tile = 128 * a + row;
+      const int tok = c.tile * p.tpt + in_tile / p.H;
+      const bool live = in_tile < p.tpt * p.H && tok < c.req.q_len;
+      if (c.k0 == 0 && c.k1 == c.nk) {
+        const int64_t grow = static_cast<int64_t>(c.req.q0 + c.tile * p.tpt) * p.H + in_tile;
+        const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+#pragma unroll 1
+        for (int q = 0; q < 256; q += 32) {  // columns 0-127 of a half: dims 128 half on; 128-255: 256 + 128 half on
+          uint32_t o[32];
+          tmem_ld32_sync(o_base + q, o);
+          uint16_t* dst = p.out + grow * kDv + 128 * half + (q & 127) + 256 * (q >> 7);
+#pragma unroll
+          for (int e = 0; e < 2 && live; ++e) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[i] = pack_bf16(__uint_as_float(o[16 * e + 2 * i]) * inv, __uint_as_float(o[16 * e + 2 * i + 1]) * inv);
+            if (p.out32) {
+              st_global_v8(dst + 16 * e, w);
+            } else {
+              reinterpret_cast<uint4*>(dst + 16 * e)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(dst + 16 * e)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+          __syncwarp();
+        }
+        if (live && half == 0 && p.lse != nullptr) p.lse[grow] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
+      } else {
+        const int slot = 2 * quad + (c.k0 > 0 ? 0 : 1);
+        float4* dst = p.o_part + (static_cast<int64_t>(2 * slot + a) * 128 + 64 * half) * 128 + row;
+#pragma unroll 1
+        for (int q = 0; q < 256; q += 32) {
+          uint32_t o[32];
+          tmem_ld32_sync(o_base + q, o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[(q / 4 + i) * 128] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        }
+        if (half == 0) p.ml_part[slot * 256 + in_tile] = ml;
+        if (c.k0 == 0 && rank == 2 && tid == 0) {
+          // runs that hold the rest of this row tile
+          const int64_t at = s->run.end - c.left;
+          const int last = static_cast<int>((at + c.nk - 1) / s->run.per);
+          const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt) - c.tile * p.tpt) * p.H;
+          p.desc[quad] = make_int4((c.req.q0 + c.tile * p.tpt) * p.H, rows, last - quad, 0);
+        }
+      }
+      tc_fence_before();
+    }
+    if (p.cut && rank == 2 && tid == 0) {
+      // nothing to join: no row tile that starts in this run goes on behind it
+      if (!ok || s->run.pos >= s->run.end || c.k0 > 0 || c.k1 == c.nk) p.desc[quad] = make_int4(0, 0, 0, 0);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (s->abort) {
+    // a wait ran out: let copies and MMAs in flight end before the memory they use is given up
+    const long long t0 = clock64();
+    while (clock64() - t0 < 20000000ll) __nanosleep(1000);
+  }
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+FuncAttrOnce g_smem;
+std::atomic<int> g_quads[kMaxDeviceOrdinals];  // clusters at once + 1, 0 = not asked yet
+
+void config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int quads, cudaStream_t s) {
+  *cfg = {};
+  cfg->gridDim = dim3(static_cast<unsigned>(4 * quads));
+  cfg->blockDim = dim3(kThreads);
+  cfg->dynamicSmemBytes = kSmTotal;
+  cfg->stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 4;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+}
+
+}  // namespace
+
+int num_quads(bool f8) {
+  int dev = 0;
+  if (f8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDeviceOrdinals) return 0;
+  int n = g_quads[dev].load(std::memory_order_acquire);
+  if (n == 0) {
+    int clusters = 0;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    config(&cfg, attr, 1, nullptr);
+    cfg.numAttrs = 1;
+    if (allow_smem(dense_mla_quad_kernel, kSmTotal, g_smem) != DSA_OK ||
+        cudaOccupancyMaxActiveClusters(&clusters, dense_mla_quad_kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      clusters = 0;
+    }
+    n = std::min(clusters, num_sms() / 4) + 1;
+    g_quads[dev].store(n, std::memory_order_release);
+  }
+  return n - 1;
+}
+
+dsa_status_t launch_quads(const DenseParams& p, bool f8, const void* q, const void* kv, int quads, cudaStream_t s) {
+  (void)f8;
+  CUtensorMap qmap, kvmap, ropemap, rowmap;
+  const uint64_t rows = static_cast<uint64_t>(p.total_rows);
+  const uint64_t strides[2] = {kDk * 2, 128};  // rows of 9 blocks of 64 dims, block-major boxes
+  const uint64_t qdims[3] = {64, static_cast<uint64_t>(p.T) * p.H, 9}, kvdims[3] = {64, rows, 9}, rowdims[2] = {kDk, rows};
+  const uint32_t qbox[3] = {64, 128, 1}, kvbox[3] = {64, 64, 2}, ropebox[3] = {64, 64, 1}, rowbox[2] = {64, 1};
+  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  dsa_status_t st;
+  if ((st = make_tmap(&qmap, bf16, 3, q, qdims, strides, qbox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&kvmap, bf16, 3, kv, kvdims, strides, kvbox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&ropemap, bf16, 3, kv, kvdims, strides, ropebox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&rowmap, bf16, 2, kv, rowdims, strides, rowbox, sw)) != DSA_OK) return st;
+  if ((st = allow_smem(dense_mla_quad_kernel, kSmTotal, g_smem)) != DSA_OK) return st;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  config(&cfg, attr, quads, s);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_quad_kernel, p, qmap, kvmap, ropemap, rowmap);
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_quad_kernel launch failed: %s", cudaGetErrorString(e));
+  return DSA_OK;
+}
+
+}  // namespace dense
+}  // namespace dsa
