@@ -24,18 +24,19 @@ namespace dense {
 namespace {
 
 constexpr int kWorkers = 8;  // warps 0-7: softmax (CTAs 0, 1), rescaling and results (CTAs 2, 3)
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kThreads = 320;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kSendWarp = 10, kThreads = 352;  // 10: CTAs 0, 1 only
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColQ = 256;  // CTAs 0, 1: S 2 x 128, q 256; CTAs 2, 3: O 512
 
-// Shared memory. CTAs 0, 1: a ring of 13 slots of 16 KB (q's 8 latent blocks of
+// Shared memory. CTAs 0, 1: a ring of 11 slots of 16 KB (q's 8 latent blocks of
 // 128 rows x 64 dims when a row tile begins, then per step 4 slots of 64 keys
-// x 128 dims and one of 64 keys x 64 rope dims), q's rope block, row maxima.
+// x 128 dims and one of 64 keys x 64 rope dims), q's rope block, P and factors
+// on their way to CTA 2 + a, row maxima.
 // CTAs 2, 3: a ring of 10 slots (per step 4 of 64 keys x 128 dims), P as two
 // buffers of 2 blocks of 128 rows x 64 keys, factors, (max, sum).
-constexpr int kRingS = 13, kRingV = 10;
-constexpr int kSmRopeQ = kRingS * kSlot, kSmRed = kSmRopeQ + 16384;
+constexpr int kRingS = 11, kRingV = 10;
+constexpr int kSmRopeQ = kRingS * kSlot, kSmPOut = kSmRopeQ + 16384, kSmRed = kSmPOut + 32768, kSmAlphaOut = kSmRed + 2048;
 constexpr int kSmP = kRingV * kSlot, kSmAlpha = kSmP + 2 * 32768, kSmMl = kSmAlpha + 2 * 128 * 4;
-constexpr int kSmBar = kSmRed + 2048, kSmTotal = kSmBar + 1024;
+constexpr int kSmBar = kSmAlphaOut + 512, kSmTotal = kSmBar + 512;
 static_assert(kSmTotal <= 232448 && kSmMl + 1024 <= kSmBar, "shared memory");
 
 struct Bars {  // at the same offset in every CTA
@@ -45,10 +46,11 @@ struct Bars {  // at the same offset in every CTA
   uint64_t q_ready;           // ... by both CTAs' (CTA 0's barrier)
   uint64_t rope_free;         // the row tile's last S has read q's rope block
   uint64_t s_full[2], s_free[2];  // S complete; S read by both CTAs' warps (CTA 0's barrier)
-  uint64_t rows[4];           // the two warps that share 32 rows
+  uint64_t maxima;            // every warp has written its rows' maxima (or sums)
+  uint64_t staged, sent;      // ... its part of P; P has been read by the copy to CTA 2 + a
   uint64_t ml_free;           // CTA 2 + a has read the row tile's (max, sum)
   // CTAs 2, 3
-  uint64_t p_full[2], p_ready[2];  // P landed; P fenced and O rescaled in both CTAs (CTA 2's barrier)
+  uint64_t p_full[2], p_ready[2];  // P landed; O rescaled in both CTAs (CTA 2's barrier)
   uint64_t ml_full;
   // all: O += P V of a step complete, i.e. the P buffer is free
   uint64_t pv_done[2];
@@ -56,7 +58,7 @@ struct Bars {  // at the same offset in every CTA
   volatile int abort;
   Run run;
 };
-static_assert(sizeof(Bars) <= 1024, "barrier block too large");
+static_assert(sizeof(Bars) <= 512, "barrier block too large");
 
 __device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t ctas) {
   asm volatile(
@@ -72,10 +74,16 @@ __device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tme
       "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "r"(bdesc_lo), "r"(bdesc_hi), "r"(idesc), "r"(accumulate));
 }
-__device__ __forceinline__ void st_async_b32(uint32_t cluster_addr, uint32_t cluster_bar, uint32_t a) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr), "r"(a),
-               "r"(cluster_bar)
+// Bulk copy from this CTA's shared memory into another's, counted on a barrier
+// there; bulk_read_done: the sources of this thread's copies may be overwritten.
+__device__ __forceinline__ void bulk_copy_s2c(uint32_t cluster_dst, uint32_t src, uint32_t bytes, uint32_t cluster_bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   cluster_dst),
+               "r"(src), "r"(bytes), "r"(cluster_bar)
                : "memory");
+}
+__device__ __forceinline__ void bulk_read_done() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void st_async_v2(uint32_t cluster_addr, uint32_t cluster_bar, uint32_t a, uint32_t b) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(cluster_addr),
@@ -132,7 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
       mbar_init(&s->p_ready[i], 2 * kWorkers);
       mbar_init(&s->pv_done[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&s->rows[i], 2);
+    mbar_init(&s->maxima, kWorkers);
+    mbar_init(&s->staged, kWorkers);
+    mbar_init(&s->sent, 1);
     mbar_init(&s->ml_free, kWorkers);
     mbar_init(&s->ml_full, 1);
     fence_mbar_init();
@@ -327,6 +337,32 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
       if (!ok && lane == 0) abort_now();
     }
     __syncwarp();
+  } else if (warp == kSendWarp) {
+    // ---------------- P and the factors of each step to CTA 2 + a
+    if (!values) {
+      const uint32_t p_dst = in_cta(smem + kSmP, 2 + a), p_full = in_cta(&s->p_full[0], 2 + a);
+      const uint32_t alpha_dst = in_cta(smem + kSmAlpha, 2 + a);
+      bool ok = true;
+      int it = 0;
+      for (bool more = c.start(p, &s->run); more && ok; more = c.next(p)) {
+        for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
+          const int buf = it & 1;
+          // P is staged, and its buffer there is free: PV of the step before the last is done
+          ok = warp_wait(&s->staged, it & 1) && (it < 2 || warp_wait(&s->pv_done[buf], ((it >> 1) - 1) & 1));
+          if (!ok) {
+            if (lane == 0) abort_now();
+            break;
+          }
+          if (lane == 0) {
+            bulk_copy_s2c(p_dst + buf * 32768, smem_u32(smem + kSmPOut), 32768, p_full + 8 * buf);
+            bulk_copy_s2c(alpha_dst + buf * 512, smem_u32(smem + kSmAlphaOut), 512, p_full + 8 * buf);
+            bulk_read_done();
+            mbar_arrive(&s->sent);
+          }
+          __syncwarp();
+        }
+      }
+    }
   } else if (!values) {
     // ---------------- softmax: TMEM lane = row; the two warps of a lane group
     // take 64 keys each
@@ -334,16 +370,15 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     float* red = reinterpret_cast<float*>(smem + kSmRed);  // [step parity][half][row]
     const uint32_t q_ready = in_cta(&s->q_ready, 0), s_free = in_cta(&s->s_free[0], 0);
-    const uint32_t p_dst = in_cta(smem + kSmP, 2 + a) + half * 16384, p_full = in_cta(&s->p_full[0], 2 + a);
-    const uint32_t alpha_dst = in_cta(smem + kSmAlpha, 2 + a) + row * 4;
+    uint8_t* p_out = smem + kSmPOut + half * 16384;
     Ring<kRingS> ring;
     bool ok = true;
     int it = 0, seg = 0;
     uint32_t meets = 0;
-    const auto meet = [&] {  // the two warps that hold the same rows: what each wrote is seen by both
+    const auto meet = [&] {  // what every warp wrote is seen by all
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s->rows[warp & 3]);
-      return warp_wait(&s->rows[warp & 3], meets++ & 1);
+      if (lane == 0) mbar_arrive(&s->maxima);
+      return warp_wait(&s->maxima, meets++ & 1);
     };
     for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
       // q's latent dims -> tensor memory (the A operand); its slots are then free
@@ -408,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
           uint32_t v[32];
           tmem_ld32_sync(lane_base + kColS + 128 * buf + 64 * half + 32 * h, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sc[32 * h + i] = __uint_as_float(v[i]) * p.scale_log2;
+          for (int i = 0; i < 32; ++i) sc[32 * h + i] = __uint_as_float(v[i]);
         }
         tc_fence_before();
         __syncwarp();
@@ -422,23 +457,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
         for (int i = 1; i < 64; ++i) mt = fmaxf(mt, sc[i]);
         float* rd = red + buf * 256;
         rd[half * 128 + row] = mt;
-        if (!meet()) {
+        // ... and P's staging memory is free: the last step's copy has read it. (PV
+        // of that step need not be done; the wait is for this SM's reads only.)
+        if (it > 0 && !warp_wait(&s->sent, (it - 1) & 1)) ok = false;
+        if (!ok || !meet()) {
           if (lane == 0) abort_now();
           ok = false;
           break;
         }
-        mt = fmaxf(rd[row], rd[128 + row]);
+        mt = fmaxf(rd[row], rd[128 + row]) * p.scale_log2;
         const bool rescale = mt > m + kRescaleThreshold;
         const float m_new = rescale ? mt : m, neg_m = -m_new;
         const float alpha = rescale ? ex2_approx(m - m_new) : 1.f;
         m = m_new;
-        // P's buffer is free once PV of the step before the last is done
-        if (it >= 2 && !warp_wait(&s->pv_done[buf], ((it >> 1) - 1) & 1)) {
-          if (lane == 0) abort_now();
-          ok = false;
-          break;
-        }
-        const uint32_t bar = p_full + 8 * buf, dst = p_dst + buf * 32768;
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -446,14 +477,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             // the sum takes the fp32 weights; the product takes them rounded to bf16
-            const float e0 = ex2_approx(sc[8 * k + 2 * i] + neg_m), e1 = ex2_approx(sc[8 * k + 2 * i + 1] + neg_m);
+            const float e0 = ex2_approx(fmaf(sc[8 * k + 2 * i], p.scale_log2, neg_m));
+            const float e1 = ex2_approx(fmaf(sc[8 * k + 2 * i + 1], p.scale_log2, neg_m));
             s0 += e0;
             s1 += e1;
             pk[i] = pack_bf16(e0, e1);
           }
-          st_async_v4(dst + sw128_offset(row, k), bar, pk[0], pk[1], pk[2], pk[3]);
+          *reinterpret_cast<uint4*>(p_out + sw128_offset(row, k)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
-        if (half == 0) st_async_b32(alpha_dst + buf * 512, bar, __float_as_uint(alpha));
+        if (half == 0) *reinterpret_cast<float*>(smem + kSmAlphaOut + 4 * row) = alpha;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->staged);
         l = l * alpha + (s0 + s1);
       }
       if (!ok) break;
@@ -507,9 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
           if (lane == 0) abort_now();
           break;
         }
-        // the stores of the other CTA are seen here; the tensor cores read
-        // them through the async proxy
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_relaxed(p_ready + 8 * buf);
