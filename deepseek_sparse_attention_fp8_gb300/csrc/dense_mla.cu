@@ -41,7 +41,6 @@ using namespace dense;
 constexpr int kAuxWarp = 8, kMmaWarp = 9, kKeyWarp = 10, kDecodeWarps = 8;
 template <bool F8>
 constexpr int kThreadsOf = 32 * (kKeyWarp + (F8 ? kDecodeWarps : 1));
-constexpr int kAhead = 3;   // steps (fp8 cache)
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;  // O 256 columns, S 2 x 64
 
 // Shared memory: q as 9 blocks of 64 rows x 64 dims, two steps of 4 key slots,

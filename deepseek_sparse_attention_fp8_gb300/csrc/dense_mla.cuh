@@ -27,6 +27,7 @@ constexpr int kTile = 128;    // keys of a step
 constexpr int kSlot = 16384;  // 64 keys x 128 dims
 constexpr float kRescaleThreshold = 8.f;  // log2 units
 constexpr long long kWaitLimitCycles = 2000000000ll;
+constexpr int kAhead = 3;   // steps that the fp8 cache's rows are asked into L2 ahead
 constexpr int kMinRun = 4;  // steps a run has at least when row tiles may be cut
 
 struct DenseParams {

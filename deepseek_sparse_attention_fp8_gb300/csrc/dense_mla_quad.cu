@@ -23,28 +23,33 @@ namespace dsa {
 namespace dense {
 namespace {
 
-constexpr int kWorkers = 8;  // warps 0-7: softmax (CTAs 0, 1), rescaling and results (CTAs 2, 3)
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kSendWarp = 10, kThreads = 352;  // 10: CTAs 0, 1 only
+// Warps 0-7: softmax (CTAs 0, 1), rescaling and results (CTAs 2, 3); 8 TMA
+// loads, 9 MMA, 10 P on its way (CTAs 0, 1); with the fp8 cache 12-19 decode
+// keys and values (11 is idle).
+constexpr int kWorkers = 8, kLoadWarp = 8, kMmaWarp = 9, kSendWarp = 10, kDecodeWarp = 12, kDecodeWarps = 8;
+template <bool F8>
+constexpr int kThreadsOf = F8 ? 640 : 352;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColQ = 256;  // CTAs 0, 1: S 2 x 128, q 256; CTAs 2, 3: O 512
 
-// Shared memory. CTAs 0, 1: a ring of 11 slots of 16 KB (q's 8 latent blocks of
+// Shared memory. CTAs 0, 1: a ring of 10 slots of 16 KB (q's 8 latent blocks of
 // 128 rows x 64 dims when a row tile begins, then per step 4 slots of 64 keys
-// x 128 dims and one of 64 keys x 64 rope dims), q's rope block, P and factors
-// on their way to CTA 2 + a, row maxima.
+// x 128 dims), the rope dims of two steps' 64 keys, q's rope block, P and
+// factors on their way to CTA 2 + a, row maxima.
 // CTAs 2, 3: a ring of 10 slots (per step 4 of 64 keys x 128 dims), P as two
 // buffers of 2 blocks of 128 rows x 64 keys, factors, (max, sum).
-constexpr int kRingS = 11, kRingV = 10;
-constexpr int kSmRopeQ = kRingS * kSlot, kSmPOut = kSmRopeQ + 16384, kSmRed = kSmPOut + 32768, kSmAlphaOut = kSmRed + 2048;
-constexpr int kSmP = kRingV * kSlot, kSmAlpha = kSmP + 2 * 32768, kSmMl = kSmAlpha + 2 * 128 * 4;
+constexpr int kRing = 10;
+constexpr int kSmRopeK = kRing * kSlot, kSmRopeQ = kSmRopeK + 2 * 8192, kSmPOut = kSmRopeQ + 16384, kSmRed = kSmPOut + 32768, kSmAlphaOut = kSmRed + 2048;
+constexpr int kSmP = kRing * kSlot, kSmAlpha = kSmP + 2 * 32768, kSmMl = kSmAlpha + 2 * 128 * 4;
 constexpr int kSmBar = kSmAlphaOut + 512, kSmTotal = kSmBar + 512;
 static_assert(kSmTotal <= 232448 && kSmMl + 1024 <= kSmBar, "shared memory");
 
 struct Bars {  // at the same offset in every CTA
-  uint64_t full[kRingS], empty[kRingS];  // ring slots; full: of both CTAs of a pair, the even one's barrier
+  uint64_t full[kRing], empty[kRing];  // ring slots; full: of both CTAs of a pair, the even one's barrier
   // CTAs 0, 1
   uint64_t q_full, q_copied;  // q landed in the ring; copied to tensor memory by this CTA's warps
   uint64_t q_ready;           // ... by both CTAs' (CTA 0's barrier)
-  uint64_t rope_free;         // the row tile's last S has read q's rope block
+  uint64_t q_rope_free;       // the row tile's last S has read q's rope block
+  uint64_t rope_full[2];      // the rope dims of a step's keys, of both CTAs (CTA 0's barrier); free again with S
   uint64_t s_full[2], s_free[2];  // S complete; S read by both CTAs' warps (CTA 0's barrier)
   uint64_t maxima;            // every warp has written its rows' maxima (or sums)
   uint64_t staged, sent;      // ... its part of P; P has been read by the copy to CTA 2 + a
@@ -96,19 +101,20 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity
 
 // A ring position that walks its slots; every slot's empty barrier changes
 // phase once per turn (full too, but for slots that held q).
-template <int N>
 struct Ring {
   int slot = 0;
   uint32_t turn = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == N) {
-      slot = 0;
+  __device__ __forceinline__ void next(int n = 1) {
+    slot += n;
+    if (slot >= kRing) {
+      slot -= kRing;
       ++turn;
     }
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __grid_constant__ DenseParams p,
+template <bool F8>
+__global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const __grid_constant__ DenseParams p,
                                                                      const __grid_constant__ CUtensorMap qmap,
                                                                      const __grid_constant__ CUtensorMap kvmap,
                                                                      const __grid_constant__ CUtensorMap ropemap,
@@ -125,14 +131,16 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < kRingS; ++i) {
-      mbar_init(&s->full[i], 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&s->full[i], F8 ? 2 * kDecodeWarps : 1);
       mbar_init(&s->empty[i], 1);
     }
     mbar_init(&s->q_full, 1);
     mbar_init(&s->q_copied, kWorkers);
     mbar_init(&s->q_ready, 2 * kWorkers);
-    mbar_init(&s->rope_free, 1);
+    mbar_init(&s->q_rope_free, 1);
+    mbar_init(&s->rope_full[0], 1);
+    mbar_init(&s->rope_full[1], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s->s_full[i], 1);
       mbar_init(&s->s_free[i], 2 * kWorkers);
@@ -163,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
   tc_fence_after();
   const uint32_t tmem = s->tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_run<kThreads>(p, &s->run, smem, quad, n_quads);
+  plan_run<kThreadsOf<F8>>(p, &s->run, smem, quad, n_quads);
 
   const auto abort_now = [&] {
     s->abort = 1;
@@ -176,20 +184,17 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
 
   if (warp == kLoadWarp && !values) {
     // ---------------- q of each row tile, then the own keys of its steps
-    Ring<kRingS> ring;
+    // (fp8: their rope dims; the rest is decoded)
+    Ring ring;
     bool ok = true;
-    int seg = 0;
+    int it = 0, seg = 0;
     const auto claim = [&] {  // the slot's former content has been used
-      if (ring.turn > 0 && !warp_wait(&s->empty[ring.slot], (ring.turn - 1) & 1)) {
-        if (lane == 0) abort_now();
-        ok = false;
-      }
+      if (ring.turn > 0 && !warp_wait(&s->empty[ring.slot], (ring.turn - 1) & 1)) ok = false;
       return ok;
     };
     for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
       const int row0 = (c.req.q0 + c.tile * p.tpt) * p.H + 128 * a;
-      if (seg > 0 && !warp_wait(&s->rope_free, (seg - 1) & 1)) {
-        if (lane == 0) abort_now();
+      if (seg > 0 && !warp_wait(&s->q_rope_free, (seg - 1) & 1)) {
         ok = false;
         break;
       }
@@ -205,22 +210,101 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
       }
       Units u;
       u.start(p, c, lane, true);
-      for (int kt = c.k0; kt < c.k1 && ok; ++kt) {
+      Units far = u;
+      const auto ask = [&](int kt) {  // fp8: the decoding warps' loads find the rows in L2
+        const Rows x = far.get(p, c, 2 * kt + a, lane, false);
+        if (x.n > 0 && lane == 0) prefetch_l2(p.kv + static_cast<int64_t>(x.row) * kF8Row, x.n * kF8Row);
+      };
+      for (int kt = c.k0; F8 && kt < min(c.k0 + kAhead, c.k1); ++kt) ask(kt);
+      for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
+        const int buf = it & 1;
+        if (F8 && kt + kAhead < c.k1) ask(kt + kAhead);
         const Rows x = u.get(p, c, 2 * kt + a, lane, true);
-        for (int k = 0; k < 5 && claim(); ++k, ring.next()) {
-          if (a == 0 && lane == 0) mbar_arrive_expect_tx(&s->full[ring.slot], k < 4 ? 2 * kSlot : kSlot);
-          const uint32_t dst = smem_u32(smem + ring.slot * kSlot), bar = in_cta(&s->full[ring.slot], even);
-          if (k < 4) load_keys(dst, &kvmap, &rowmap, bar, x, p.total_rows, 2 * k, 2, lane);
-          else load_keys(dst, &ropemap, &rowmap, bar, x, p.total_rows, 8, 1, lane);
+        for (int k = 0; !F8 && k < 4 && claim(); ++k, ring.next()) {
+          if (a == 0 && lane == 0) mbar_arrive_expect_tx(&s->full[ring.slot], 2 * kSlot);
+          load_keys(smem_u32(smem + ring.slot * kSlot), &kvmap, &rowmap, in_cta(&s->full[ring.slot], even), x,
+                    p.total_rows, 2 * k, 2, lane);
         }
+        if (F8) ring.next(4);
+        // the rope dims: their buffer is free with S of the step before the last
+        ok = ok && (it < 2 || warp_wait(&s->s_full[buf], ((it >> 1) - 1) & 1));
+        if (!ok) break;
+        if (a == 0 && lane == 0) mbar_arrive_expect_tx(&s->rope_full[buf], 2 * 8192);
+        load_keys(smem_u32(smem + kSmRopeK + buf * 8192), &ropemap, &rowmap, in_cta(&s->rope_full[buf], even), x,
+                  p.total_rows, F8 ? 0 : 8, 1, lane);
       }
     }
+    if (!ok && lane == 0) abort_now();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else if (F8 && warp >= kDecodeWarp) {
+    // ---------------- fp8: a step's 4 slots of 64 keys x 128 dims (CTAs 0, 1:
+    // the 4 groups of the own keys; CTAs 2, 3: the 2 own groups of both units
+    // of keys), 8 keys per warp. The registers of codes that have been decoded
+    // take the same codes of the next step
+    const int lane8 = lane & 7, key = (warp - kDecodeWarp) * 8 + (lane >> 3);  // and key + 4
+    const bool swap = lane8 & 4;
+    const uint32_t blk = (lane8 >> 2) * 8192, c0 = 2 * (lane8 & 3);
+    const uint32_t at[2][2] = {{blk + sw128_offset(key, c0 + swap), blk + sw128_offset(key, c0 + !swap)},
+                               {blk + sw128_offset(key + 4, c0 + swap), blk + sw128_offset(key + 4, c0 + !swap)}};
+    const uint32_t full0 = in_cta(&s->full[0], even);
+    Ring ring;
+    Units u;
+    bool more = c.start(p, &s->run), ok = true;
+    int kt = c.k0;
+    Codes code[2][4];  // [key][slot]
+    Rows x0{0, 0}, x1{0, 0};
+    const auto locate = [&] {
+      if (kt == c.k0) u.start(p, c, lane, false);
+      x0 = u.get(p, c, 2 * kt, lane, false);
+      x1 = u.get(p, c, 2 * kt + 1, lane, false);
+      if (!values && a) x0 = x1;
+    };
+    const auto fetch = [&](int k) {
+      const Rows& x = values && k >= 2 ? x1 : x0;
+      const int group = values ? 2 * a + (k & 1) : k;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        code[i][k] = fetch16(p.kv + static_cast<int64_t>(x.row + key + 4 * i) * kF8Row, group, lane8, key + 4 * i < x.n);
+    };
+    if (more) {
+      locate();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) fetch(k);
+    }
+    while (more && ok) {
+      if (!values && kt == c.k0) ring.next(8);  // q's slots
+      if (++kt == c.k1) {
+        more = c.next(p);
+        kt = c.k0;
+      }
+      if (more) locate();
+      else x0.n = x1.n = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (ring.turn > 0 && !warp_wait(&s->empty[ring.slot], (ring.turn - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t* slot = smem + ring.slot * kSlot;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Decoded v = decode16(code[i][k], swap);
+          *reinterpret_cast<uint4*>(slot + at[i][0]) = v.first;
+          *reinterpret_cast<uint4*>(slot + at[i][1]) = v.second;
+        }
+        fetch(k);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(full0 + 8 * ring.slot);
+        ring.next();
+      }
+    }
+    if (!ok && lane == 0) abort_now();
   } else if (warp == kLoadWarp) {
     // ---------------- all keys of each step, the own value dims
-    Ring<kRingV> ring;
+    Ring ring;
     bool ok = true;
-    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p)) {
+    for (bool more = !F8 && c.start(p, &s->run); more && ok; more = c.next(p)) {
       Units u;
       u.start(p, c, lane, false);
       for (int kt = c.k0; kt < c.k1 && ok; ++kt) {
@@ -245,46 +329,46 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
       const uint32_t idesc = idesc_bf16(256, kTile, false, false);
       const uint64_t dk = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
       const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
-      Ring<kRingS> ring;
+      Ring ring;
       uint32_t phases = 0;  // of the slots' full barriers: q's uses of a slot do not count there
       bool ok = true;
       int it = 0, seg = 0;
       for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
-        for (int i = 0; i < 8; ++i) ring.next();
+        ring.next(8);
         ok = warp_wait(&s->q_ready, seg & 1);
         for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
           const int buf = it & 1;
           if (it >= 2) ok = warp_wait(&s->s_free[buf], ((it >> 1) - 1) & 1);
           const uint32_t d = tmem + kColS + 128 * buf;
 #pragma unroll 1
-          for (int k = 0; k < 5 && ok; ++k, ring.next()) {
+          for (int k = 0; k < 4 && ok; ++k, ring.next()) {
             ok = warp_wait(&s->full[ring.slot], (phases >> ring.slot) & 1);
             if (!ok) break;
             phases ^= 1u << ring.slot;
             tc_fence_after();
-            const uint32_t b0 = k_lo + ((ring.slot * kSlot) >> 4);
-            if (k < 4) {
-              const uint32_t q0 = tmem + kColQ + k * 64, acc0 = k > 0 ? 1u : 0u;
-              if (elect_one()) {
+            const uint32_t b0 = k_lo + ((ring.slot * kSlot) >> 4), q0 = tmem + kColQ + k * 64, acc0 = k > 0 ? 1u : 0u;
+            if (elect_one()) {
 #pragma unroll
-                for (int st = 0; st < 8; ++st)
-                  mma_bf16_ts_pair(d, q0 + st * 8, b0 + (((st >> 2) * 8192 + (st & 3) * 32) >> 4), k_hi, idesc,
-                                   st > 0 ? 1u : acc0);
-                commit_to(&s->empty[ring.slot], 0x3);
-              }
-            } else {
-              const bool last = kt + 1 == c.k1;
-              if (elect_one()) {
-#pragma unroll
-                for (int st = 0; st < 4; ++st)
-                  mma_bf16_ss_pair(d, k_lo + ((kSmRopeQ + st * 32) >> 4), k_hi, b0 + ((st * 32) >> 4), k_hi, idesc, 1u);
-                commit_to(&s->empty[ring.slot], 0x3);
-                commit_to(&s->s_full[buf], 0x3);
-                if (last) commit_to(&s->rope_free, 0x3);
-              }
+              for (int st = 0; st < 8; ++st)
+                mma_bf16_ts_pair(d, q0 + st * 8, b0 + (((st >> 2) * 8192 + (st & 3) * 32) >> 4), k_hi, idesc,
+                                 st > 0 ? 1u : acc0);
+              commit_to(&s->empty[ring.slot], 0x3);
             }
             __syncwarp();
           }
+          ok = ok && warp_wait(&s->rope_full[buf], (it >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t b0 = k_lo + ((kSmRopeK + buf * 8192) >> 4);
+          const bool last = kt + 1 == c.k1;
+          if (elect_one()) {
+#pragma unroll
+            for (int st = 0; st < 4; ++st)
+              mma_bf16_ss_pair(d, k_lo + ((kSmRopeQ + st * 32) >> 4), k_hi, b0 + ((st * 32) >> 4), k_hi, idesc, 1u);
+            commit_to(&s->s_full[buf], 0x3);
+            if (last) commit_to(&s->q_rope_free, 0x3);
+          }
+          __syncwarp();
         }
       }
       if (!ok && lane == 0) abort_now();
@@ -299,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
       const uint64_t dv = smem_desc(smem_u32(smem), 8192, 1024, kSwizzle128B);
       const uint32_t p_lo = static_cast<uint32_t>(dp), p_hi = static_cast<uint32_t>(dp >> 32);
       const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
-      Ring<kRingV> ring;
+      Ring ring;
       bool ok = true;
       int it = 0;
       for (bool more = c.start(p, &s->run); more && ok; more = c.next(p)) {
@@ -363,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
         }
       }
     }
-  } else if (!values) {
+  } else if (warp < kWorkers && !values) {
     // ---------------- softmax: TMEM lane = row; the two warps of a lane group
     // take 64 keys each
     const int row = (warp & 3) * 32 + lane, half = warp >> 2;
@@ -371,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
     float* red = reinterpret_cast<float*>(smem + kSmRed);  // [step parity][half][row]
     const uint32_t q_ready = in_cta(&s->q_ready, 0), s_free = in_cta(&s->s_free[0], 0);
     uint8_t* p_out = smem + kSmPOut + half * 16384;
-    Ring<kRingS> ring;
+    Ring ring;
     bool ok = true;
     int it = 0, seg = 0;
     uint32_t meets = 0;
@@ -413,12 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
           if (lane == 0) abort_now();
           break;
         }
-        if (lane < 8) mbar_arrive(&s->empty[(ring.slot + kRingS - 8 + lane) % kRingS]);
+        if (lane < 8) mbar_arrive(&s->empty[(ring.slot + kRing - 8 + lane) % kRing]);
         __syncwarp();
       }
-      for (int i = 0; i < 5 * (c.k1 - c.k0) % (kRingS); ++i) {
-        if (++ring.slot == kRingS) ring.slot = 0;
-      }
+      ring.slot = (ring.slot + 4 * ((c.k1 - c.k0) % kRing)) % kRing;  // the steps' slots
 
       const int in_tile = 128 * a + row;
       const int tok = c.tile * p.tpt + in_tile / p.H;
@@ -437,24 +519,26 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
           break;
         }
         tc_fence_after();
-        float sc[64];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        // 32 scores at a time: once for the maximum, once more for the weights,
+        // as 64 registers of them would spill beside the decoding warps'
+        const auto scores = [&](int h, float (&sc)[32]) {
           uint32_t v[32];
           tmem_ld32_sync(lane_base + kColS + 128 * buf + 64 * half + 32 * h, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sc[32 * h + i] = __uint_as_float(v[i]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote_relaxed(s_free + 8 * buf);
-        if (n < 64) {
+          for (int i = 0; i < 32; ++i) sc[i] = __uint_as_float(v[i]);
+          if (n < 32 * h + 32) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) sc[i] = i < n ? sc[i] : -INFINITY;
-        }
-        float mt = sc[0];
+            for (int i = 0; i < 32; ++i) sc[i] = 32 * h + i < n ? sc[i] : -INFINITY;
+          }
+        };
+        float mt = -INFINITY;
 #pragma unroll
-        for (int i = 1; i < 64; ++i) mt = fmaxf(mt, sc[i]);
+        for (int h = 0; h < 2; ++h) {
+          float sc[32];
+          scores(h, sc);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mt = fmaxf(mt, sc[i]);
+        }
         float* rd = red + buf * 256;
         rd[half * 128 + row] = mt;
         // ... and P's staging memory is free: the last step's copy has read it. (PV
@@ -472,18 +556,28 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
         m = m_new;
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // the sum takes the fp32 weights; the product takes them rounded to bf16
-            const float e0 = ex2_approx(fmaf(sc[8 * k + 2 * i], p.scale_log2, neg_m));
-            const float e1 = ex2_approx(fmaf(sc[8 * k + 2 * i + 1], p.scale_log2, neg_m));
-            s0 += e0;
-            s1 += e1;
-            pk[i] = pack_bf16(e0, e1);
+        for (int h = 0; h < 2; ++h) {
+          float sc[32];
+          scores(h, sc);
+          if (h == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_relaxed(s_free + 8 * buf);
           }
-          *reinterpret_cast<uint4*>(p_out + sw128_offset(row, k)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // the sum takes the fp32 weights; the product takes them rounded to bf16
+              const float e0 = ex2_approx(fmaf(sc[8 * k + 2 * i], p.scale_log2, neg_m));
+              const float e1 = ex2_approx(fmaf(sc[8 * k + 2 * i + 1], p.scale_log2, neg_m));
+              s0 += e0;
+              s1 += e1;
+              pk[i] = pack_bf16(e0, e1);
+            }
+            *reinterpret_cast<uint4*>(p_out + sw128_offset(row, 4 * h + k)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
         }
         if (half == 0) *reinterpret_cast<float*>(smem + kSmAlphaOut + 4 * row) = alpha;
         fence_proxy_async_smem();
@@ -506,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
       if (half == 0)
         st_async_v2(in_cta(smem + kSmMl, 2 + a) + row * 8, in_cta(&s->ml_full, 2 + a), __float_as_uint(m), __float_as_uint(l));
     }
-  } else {
+  } else if (warp < kWorkers) {
     // ---------------- O: rescaling when a row's maximum has grown, and the
     // results; TMEM lane = row, the two warps of a lane group take 256 columns each
     const int row = (warp & 3) * 32 + lane, half = warp >> 2;
@@ -629,13 +723,14 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_quad_kernel(const __gri
   if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-FuncAttrOnce g_smem;
-std::atomic<int> g_quads[kMaxDeviceOrdinals];  // clusters at once + 1, 0 = not asked yet
+FuncAttrOnce g_smem[2];
+std::atomic<int> g_quads[2][kMaxDeviceOrdinals];  // clusters at once + 1, 0 = not asked yet
 
+template <bool F8>
 void config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int quads, cudaStream_t s) {
   *cfg = {};
   cfg->gridDim = dim3(static_cast<unsigned>(4 * quads));
-  cfg->blockDim = dim3(kThreads);
+  cfg->blockDim = dim3(kThreadsOf<F8>);
   cfg->dynamicSmemBytes = kSmTotal;
   cfg->stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -648,50 +743,65 @@ void config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int quads, cudaS
   cfg->numAttrs = 2;
 }
 
+template <bool F8>
+int clusters_at_once() {
+  int clusters = 0;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  config<F8>(&cfg, attr, 1, nullptr);
+  cfg.numAttrs = 1;
+  if (allow_smem(dense_mla_quad_kernel<F8>, kSmTotal, g_smem[F8]) != DSA_OK ||
+      cudaOccupancyMaxActiveClusters(&clusters, dense_mla_quad_kernel<F8>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    clusters = 0;
+  }
+  return std::min(clusters, num_sms() / 4);
+}
+
+template <bool F8>
+dsa_status_t launch(const DenseParams& p, const void* q, const void* kv, int quads, cudaStream_t s) {
+  CUtensorMap qmap, kvmap, ropemap, rowmap;
+  const uint64_t rows = static_cast<uint64_t>(p.total_rows);
+  // rows of 9 blocks of 64 dims, block-major boxes; fp8: the rope dims only
+  // (128 bytes from byte 528 of a row)
+  const void* base = F8 ? static_cast<const uint8_t*>(kv) + kDv + 16 : kv;
+  const uint64_t blocks = F8 ? 1 : 9, row_bytes = F8 ? kF8Row : kDk * 2;
+  const uint64_t qstrides[2] = {kDk * 2, 128}, strides[2] = {row_bytes, 128};
+  const uint64_t qdims[3] = {64, static_cast<uint64_t>(p.T) * p.H, 9}, kvdims[3] = {64, rows, blocks};
+  const uint64_t rowdims[2] = {64 * blocks, rows};
+  const uint32_t qbox[3] = {64, 128, 1}, kvbox[3] = {64, 64, F8 ? 1u : 2u}, ropebox[3] = {64, 64, 1}, rowbox[2] = {64, 1};
+  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  dsa_status_t st;
+  if ((st = make_tmap(&qmap, bf16, 3, q, qdims, qstrides, qbox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&kvmap, bf16, 3, base, kvdims, strides, kvbox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&ropemap, bf16, 3, base, kvdims, strides, ropebox, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&rowmap, bf16, 2, base, rowdims, strides, rowbox, sw)) != DSA_OK) return st;
+  if ((st = allow_smem(dense_mla_quad_kernel<F8>, kSmTotal, g_smem[F8])) != DSA_OK) return st;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  config<F8>(&cfg, attr, quads, s);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_quad_kernel<F8>, p, qmap, kvmap, ropemap, rowmap);
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_quad_kernel launch failed: %s", cudaGetErrorString(e));
+  return DSA_OK;
+}
+
 }  // namespace
 
 int num_quads(bool f8) {
   int dev = 0;
-  if (f8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDeviceOrdinals) return 0;
-  int n = g_quads[dev].load(std::memory_order_acquire);
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDeviceOrdinals) return 0;
+  std::atomic<int>& known = g_quads[f8][dev];
+  int n = known.load(std::memory_order_acquire);
   if (n == 0) {
-    int clusters = 0;
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[2];
-    config(&cfg, attr, 1, nullptr);
-    cfg.numAttrs = 1;
-    if (allow_smem(dense_mla_quad_kernel, kSmTotal, g_smem) != DSA_OK ||
-        cudaOccupancyMaxActiveClusters(&clusters, dense_mla_quad_kernel, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      clusters = 0;
-    }
-    n = std::min(clusters, num_sms() / 4) + 1;
-    g_quads[dev].store(n, std::memory_order_release);
+    n = (f8 ? clusters_at_once<true>() : clusters_at_once<false>()) + 1;
+    known.store(n, std::memory_order_release);
   }
   return n - 1;
 }
 
 dsa_status_t launch_quads(const DenseParams& p, bool f8, const void* q, const void* kv, int quads, cudaStream_t s) {
-  (void)f8;
-  CUtensorMap qmap, kvmap, ropemap, rowmap;
-  const uint64_t rows = static_cast<uint64_t>(p.total_rows);
-  const uint64_t strides[2] = {kDk * 2, 128};  // rows of 9 blocks of 64 dims, block-major boxes
-  const uint64_t qdims[3] = {64, static_cast<uint64_t>(p.T) * p.H, 9}, kvdims[3] = {64, rows, 9}, rowdims[2] = {kDk, rows};
-  const uint32_t qbox[3] = {64, 128, 1}, kvbox[3] = {64, 64, 2}, ropebox[3] = {64, 64, 1}, rowbox[2] = {64, 1};
-  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-  dsa_status_t st;
-  if ((st = make_tmap(&qmap, bf16, 3, q, qdims, strides, qbox, sw)) != DSA_OK) return st;
-  if ((st = make_tmap(&kvmap, bf16, 3, kv, kvdims, strides, kvbox, sw)) != DSA_OK) return st;
-  if ((st = make_tmap(&ropemap, bf16, 3, kv, kvdims, strides, ropebox, sw)) != DSA_OK) return st;
-  if ((st = make_tmap(&rowmap, bf16, 2, kv, rowdims, strides, rowbox, sw)) != DSA_OK) return st;
-  if ((st = allow_smem(dense_mla_quad_kernel, kSmTotal, g_smem)) != DSA_OK) return st;
-  cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[2];
-  config(&cfg, attr, quads, s);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_quad_kernel, p, qmap, kvmap, ropemap, rowmap);
-  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_quad_kernel launch failed: %s", cudaGetErrorString(e));
-  return DSA_OK;
+  return f8 ? launch<true>(p, q, kv, quads, s) : launch<false>(p, q, kv, quads, s);
 }
 
 }  // namespace dense
