@@ -131,19 +131,17 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
     // step before, as soon as S no longer needs the dims they replace
     const int lane8 = lane & 7, key = (warp - kKeyWarp) * 8 + (lane >> 3);  // and key + 4
     const bool swap = lane8 & 4;
-    // the two chunks of key (key + 4: 4 rows and a flipped chunk bit further)
+    // the two chunks of key (key + 4: 4 rows of 128 bytes further, chunk bit 2 flipped)
     const uint32_t blk = (lane8 >> 2) * 8192, c0 = 2 * (lane8 & 3);
-    const uint32_t at[2][2] = {{blk + sw128_offset(key, c0 + swap), blk + sw128_offset(key, c0 + !swap)},
-                               {blk + sw128_offset(key + 4, c0 + swap), blk + sw128_offset(key + 4, c0 + !swap)}};
+    const uint32_t at0 = blk + sw128_offset(key, c0 + swap), at1 = blk + sw128_offset(key, c0 + !swap);
     const auto store = [&](uint8_t* slot, int i, const Decoded& v) {
-      *reinterpret_cast<uint4*>(slot + at[i][0]) = v.first;
-      *reinterpret_cast<uint4*>(slot + at[i][1]) = v.second;
+      *reinterpret_cast<uint4*>(slot + (i ? (at0 + 512) ^ 64 : at0)) = v.first;
+      *reinterpret_cast<uint4*>(slot + (i ? (at1 + 512) ^ 64 : at1)) = v.second;
     };
-    const uint32_t full0 = even(&s->full[0][0]), other0 = even(&s->other[0][r ^ 1]);
     Cursor c;
     bool more = c.start(p, &s->run), ok = true;
     int kt = c.k0;
-    Codes own[2][2], oth[2][2];  // [key][group]
+    CodePair own[2], oth[2];  // [key]
     Rows x{0, 0}, xo{0, 0};
     Units u;
     const bool rep = warp == kKeyWarp && r == 0;
@@ -157,16 +155,14 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint8_t* row = p.kv + static_cast<int64_t>(x.row + key + 4 * i) * kF8Row;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) own[i][g] = fetch16(row, 2 * h + g, lane8, key + 4 * i < x.n);
+        own[i] = fetch_pair(row, 2 * h, lane8, key + 4 * i < x.n);
       }
     };
     const auto fetch_other = [&](const Rows& xo) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint8_t* row = p.kv + static_cast<int64_t>(xo.row + key + 4 * i) * kF8Row;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) oth[i][g] = fetch16(row, 2 * r + g, lane8, key + 4 * i < xo.n);
+        oth[i] = fetch_pair(row, 2 * r, lane8, key + 4 * i < xo.n);
       }
     };
     if (more) {
@@ -188,11 +184,11 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(oth[i][g], swap));
+            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(oth[i], g, swap));
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote_relaxed(other0 + b1 * 16);
+          if (lane == 0) mbar_arrive_remote_relaxed(even(&s->other[b1][r ^ 1]));
           other_left = false;
         } else if (h < 2 && (it < 2 || all(mbar_test_wait(h == 0 ? &s->pv_half[buf] : &s->pv_done[buf],
                                                           ((it >> 1) - 1) & 1)))) {
@@ -200,11 +196,11 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(own[i][g], swap));
+            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(own[i], g, swap));
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane < 2) mbar_arrive_remote_relaxed(full0 + (buf * 4 + 2 * h + lane) * 8);
+          if (lane < 2) mbar_arrive_remote_relaxed(even(&s->full[buf][2 * h + lane]));
           ++h;
           if (h == 2) {
             if (++kt == c.k1) {

@@ -247,31 +247,34 @@ __device__ __forceinline__ uint32_t decode2(uint32_t two, float sc) {
 __device__ __forceinline__ uint4 decode8(uint32_t a, uint32_t b, float sc) {
   return make_uint4(decode2(a, sc), decode2(a >> 16, sc), decode2(b, sc), decode2(b >> 16, sc));
 }
-struct Codes {
-  uint4 c;
-  float sc;
+// 16 codes (lane8: which) of each of two neighbouring groups of a key, none
+// where the key does not exist. The upper four lanes of a key write another
+// 64-dim block than the lower four, in the same banks: they store their two
+// 16-byte chunks in the other order.
+struct CodePair {
+  uint4 c[2];
+  float2 sc;
 };
-// 16 codes of a key's group (lane8: which), none where the key does not exist.
-// The upper four lanes of a key write another 64-dim block than the lower
-// four, in the same banks: they hold and store their two 16-byte chunks in the
-// other order.
-__device__ __forceinline__ Codes fetch16(const uint8_t* row, int group, int lane8, bool exists) {
-  Codes v{make_uint4(0u, 0u, 0u, 0u), 0.f};
+__device__ __forceinline__ CodePair fetch_pair(const uint8_t* row, int group, int lane8, bool exists) {
+  CodePair v{{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, make_float2(0.f, 0.f)};
   if (exists) {
     // volatile: issued here, ahead of the waits, not where the values are used
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.c.x), "=r"(v.c.y), "=r"(v.c.z), "=r"(v.c.w)
-                 : "l"(row + 128 * group + 16 * lane8));
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v.sc) : "l"(row + kDv + 4 * group));
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.c[g].x), "=r"(v.c[g].y), "=r"(v.c[g].z), "=r"(v.c[g].w)
+                   : "l"(row + 128 * (group + g) + 16 * lane8));
+    asm volatile("ld.global.nc.v2.f32 {%0, %1}, [%2];" : "=f"(v.sc.x), "=f"(v.sc.y) : "l"(row + kDv + 4 * group));
   }
   return v;
 }
 struct Decoded {
   uint4 first, second;
 };
-__device__ __forceinline__ Decoded decode16(const Codes& v, bool swap) {
-  return {decode8(swap ? v.c.z : v.c.x, swap ? v.c.w : v.c.y, v.sc),
-          decode8(swap ? v.c.x : v.c.z, swap ? v.c.y : v.c.w, v.sc)};
+__device__ __forceinline__ Decoded decode16(const CodePair& v, int g, bool swap) {
+  const uint4& c = v.c[g];
+  const float sc = g ? v.sc.y : v.sc.x;
+  return {decode8(swap ? c.z : c.x, swap ? c.w : c.y, sc), decode8(swap ? c.x : c.z, swap ? c.y : c.w, sc)};
 }
 
 // Run `index` of n_runs: every CTA sums the requests' steps itself. `scratch`

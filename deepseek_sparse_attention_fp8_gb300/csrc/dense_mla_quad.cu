@@ -244,14 +244,13 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
     const int lane8 = lane & 7, key = (warp - kDecodeWarp) * 8 + (lane >> 3);  // and key + 4
     const bool swap = lane8 & 4;
     const uint32_t blk = (lane8 >> 2) * 8192, c0 = 2 * (lane8 & 3);
-    const uint32_t at[2][2] = {{blk + sw128_offset(key, c0 + swap), blk + sw128_offset(key, c0 + !swap)},
-                               {blk + sw128_offset(key + 4, c0 + swap), blk + sw128_offset(key + 4, c0 + !swap)}};
+    const uint32_t at0 = blk + sw128_offset(key, c0 + swap), at1 = blk + sw128_offset(key, c0 + !swap);
     const uint32_t full0 = in_cta(&s->full[0], even);
     Ring ring;
     Units u;
     bool more = c.start(p, &s->run), ok = true;
     int kt = c.k0;
-    Codes code[2][4];  // [key][slot]
+    CodePair code[2][2];  // [key][pair of slots]
     Rows x0{0, 0}, x1{0, 0};
     const auto locate = [&] {
       if (kt == c.k0) u.start(p, c, lane, false);
@@ -259,17 +258,17 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
       x1 = u.get(p, c, 2 * kt + 1, lane, false);
       if (!values && a) x0 = x1;
     };
-    const auto fetch = [&](int k) {
-      const Rows& x = values && k >= 2 ? x1 : x0;
-      const int group = values ? 2 * a + (k & 1) : k;
+    const auto fetch = [&](int h) {
+      const Rows& x = values && h ? x1 : x0;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        code[i][k] = fetch16(p.kv + static_cast<int64_t>(x.row + key + 4 * i) * kF8Row, group, lane8, key + 4 * i < x.n);
+        code[i][h] = fetch_pair(p.kv + static_cast<int64_t>(x.row + key + 4 * i) * kF8Row, values ? 2 * a : 2 * h, lane8,
+                                key + 4 * i < x.n);
     };
     if (more) {
       locate();
-#pragma unroll
-      for (int k = 0; k < 4; ++k) fetch(k);
+      fetch(0);
+      fetch(1);
     }
     while (more && ok) {
       if (!values && kt == c.k0) ring.next(8);  // q's slots
@@ -280,23 +279,28 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
       if (more) locate();
       else x0.n = x1.n = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (ring.turn > 0 && !warp_wait(&s->empty[ring.slot], (ring.turn - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        uint8_t* slot = smem + ring.slot * kSlot;
+      for (int h = 0; h < 2; ++h) {
+        int slot[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const Decoded v = decode16(code[i][k], swap);
-          *reinterpret_cast<uint4*>(slot + at[i][0]) = v.first;
-          *reinterpret_cast<uint4*>(slot + at[i][1]) = v.second;
+        for (int g = 0; g < 2; ++g, ring.next()) {
+          slot[g] = ring.slot;
+          ok = ok && (ring.turn == 0 || warp_wait(&s->empty[ring.slot], (ring.turn - 1) & 1));
         }
-        fetch(k);
+        if (!ok) break;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint8_t* dst = smem + slot[g] * kSlot;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const Decoded v = decode16(code[i][h], g, swap);
+            *reinterpret_cast<uint4*>(dst + (i ? (at0 + 512) ^ 64 : at0)) = v.first;
+            *reinterpret_cast<uint4*>(dst + (i ? (at1 + 512) ^ 64 : at1)) = v.second;
+          }
+        }
+        fetch(h);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_relaxed(full0 + 8 * ring.slot);
-        ring.next();
+        if (lane < 2) mbar_arrive_remote_relaxed(full0 + 8 * (lane ? slot[1] : slot[0]));
       }
     }
     if (!ok && lane == 0) abort_now();
@@ -541,10 +545,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
         }
         float* rd = red + buf * 256;
         rd[half * 128 + row] = mt;
-        // ... and P's staging memory is free: the last step's copy has read it. (PV
-        // of that step need not be done; the wait is for this SM's reads only.)
-        if (it > 0 && !warp_wait(&s->sent, (it - 1) & 1)) ok = false;
-        if (!ok || !meet()) {
+        if (!meet()) {
           if (lane == 0) abort_now();
           ok = false;
           break;
@@ -555,6 +556,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
         const float alpha = rescale ? ex2_approx(m - m_new) : 1.f;
         m = m_new;
         float s0 = 0.f, s1 = 0.f;
+        uint32_t pk[32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float sc[32];
@@ -565,20 +567,25 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
             if (lane == 0) mbar_arrive_remote_relaxed(s_free + 8 * buf);
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // the sum takes the fp32 weights; the product takes them rounded to bf16
-              const float e0 = ex2_approx(fmaf(sc[8 * k + 2 * i], p.scale_log2, neg_m));
-              const float e1 = ex2_approx(fmaf(sc[8 * k + 2 * i + 1], p.scale_log2, neg_m));
-              s0 += e0;
-              s1 += e1;
-              pk[i] = pack_bf16(e0, e1);
-            }
-            *reinterpret_cast<uint4*>(p_out + sw128_offset(row, 4 * h + k)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          for (int i = 0; i < 16; ++i) {
+            // the sum takes the fp32 weights; the product takes them rounded to bf16
+            const float e0 = ex2_approx(fmaf(sc[2 * i], p.scale_log2, neg_m));
+            const float e1 = ex2_approx(fmaf(sc[2 * i + 1], p.scale_log2, neg_m));
+            s0 += e0;
+            s1 += e1;
+            pk[16 * h + i] = pack_bf16(e0, e1);
           }
         }
+        // P's staging memory is free once the last step's copy has read it
+        if (it > 0) ok = warp_wait(&s->sent, (it - 1) & 1);
+        if (!ok) {
+          if (lane == 0) abort_now();
+          break;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(p_out + sw128_offset(row, k)) =
+              make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
         if (half == 0) *reinterpret_cast<float*>(smem + kSmAlphaOut + 4 * row) = alpha;
         fence_proxy_async_smem();
         __syncwarp();
