@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
   float* red = reinterpret_cast<float*>(smem + kSmRed);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = static_cast<int>(cluster_ctarank());
-  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 1;
 
   if (smem_u32(smem) & 1023u) {  // the tiles need it (without static arrays the dynamic part starts there)
     if (tid == 0) report(p.dev_status, DSA_DEVERR_TIMEOUT);
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
   tc_fence_after();
   const uint32_t tmem = s->tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_run<kThreadsOf<F8>>(p, &s->run, smem + kSmKv, pair, n_pairs);
+  plan_run<kThreadsOf<F8>, false>(p, &s->run, smem + kSmKv, pair);
 
   const auto abort_now = [&] {
     s->abort = 1;
@@ -566,16 +566,15 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
           const int64_t at = s->run.end - c.left;
           const int last = static_cast<int>((at + c.nk - 1) / s->run.per);
           const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt) - c.tile * p.tpt) * p.H;
-          p.desc[pair] = make_int4((c.req.q0 + c.tile * p.tpt) * p.H, rows, last - pair, 0);
+          p.desc[pair] = make_int4((c.req.q0 + c.tile * p.tpt) * p.H, rows, last - pair, kPairTile);
         }
       }
       tc_fence_before();
     }
-    if (p.cut && r == 0 && tid == 0 && ok) {
+    if (p.cut && r == 0 && tid == 0 && s->run.mine) {
       // nothing to join: no row tile that starts in this run goes on behind it
-      if (s->run.pos >= s->run.end || c.k0 > 0 || c.k1 == c.nk) p.desc[pair] = make_int4(0, 0, 0, 0);
+      if (!ok || s->run.pos >= s->run.end || c.k0 > 0 || c.k1 == c.nk) p.desc[pair] = make_int4(0, 0, 0, 0);
     }
-    if (p.cut && r == 0 && tid == 0 && !ok) p.desc[pair] = make_int4(0, 0, 0, 0);
   }
 
   tc_fence_before();
@@ -593,16 +592,14 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_kernel(const __gr
 // Joins the partials of the row tile that starts in run blockIdx.y and goes on
 // behind it: out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j. A thread takes
 // 16 columns, i.e. dims, of a row: one 32-byte sector of the result. Partials
-// lie as the accumulators do in tensor memory: QUAD 512 columns of 128 rows per
-// CTA, else 256 columns with a row's upper dims in lane + 64.
+// lie as the accumulators do in tensor memory: the four-CTA kernel's in 512
+// columns of 128 rows per CTA, the pair kernel's in 256 columns, a row's upper
+// dims in lane + 64.
 template <bool QUAD>
-__global__ void __launch_bounds__(128) dense_mla_merge_kernel(const __grid_constant__ DenseParams p) {
+__device__ __forceinline__ void merge_tile(const DenseParams& p, const int4 d, int run) {
   constexpr int kRows = QUAD ? 256 : 128, kGroups = QUAD ? 32 : 16;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int run = blockIdx.y;
-  const int4 d = p.desc[run];
-  if (d.z <= 0) return;
   const int r = blockIdx.x / kGroups, g = blockIdx.x % kGroups;  // CTA, 16 columns
+  if (r > 1) return;
   const int lane = threadIdx.x, in_tile = QUAD ? 128 * r + lane : 64 * r + (lane & 63);
   const int dim = QUAD ? 128 * (g >> 4) + 16 * (g & 7) + ((g >> 3) & 1) * 256 : 256 * (lane >> 6) + 16 * g;
   if (in_tile >= d.y) return;
@@ -639,7 +636,15 @@ __global__ void __launch_bounds__(128) dense_mla_merge_kernel(const __grid_const
   if (dim == 0 && p.lse != nullptr) p.lse[row] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
-FuncAttrOnce g_smem_dense[2], g_smem_merge[2];
+__global__ void __launch_bounds__(128) dense_mla_merge_kernel(const __grid_constant__ DenseParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 d = p.desc[blockIdx.y];
+  if (d.z <= 0) return;
+  if (d.w == kQuadTile) merge_tile<true>(p, d, blockIdx.y);
+  else merge_tile<false>(p, d, blockIdx.y);
+}
+
+FuncAttrOnce g_smem_dense[2], g_smem_merge;
 
 int num_pairs() { return std::max(1, num_sms() / 2); }
 // partials of 128 rows per pair; a quad's 256 rows take two pairs' worth, and
@@ -687,12 +692,11 @@ dsa_status_t launch_dense(const DenseParams& p, const void* q, const void* kv, i
   return DSA_OK;
 }
 
-template <bool QUAD>
-dsa_status_t launch_merge(const DenseParams& p, int runs, cudaStream_t s) {
-  dsa_status_t st = allow_smem(dense_mla_merge_kernel<QUAD>, 0, g_smem_merge[QUAD]);
+dsa_status_t launch_merge(const DenseParams& p, cudaStream_t s) {
+  dsa_status_t st = allow_smem(dense_mla_merge_kernel, 0, g_smem_merge);
   if (st != DSA_OK) return st;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(QUAD ? 64 : 32, static_cast<unsigned>(runs));
+  cfg.gridDim = dim3(p.quads > 0 ? 64 : 32, static_cast<unsigned>(p.pairs));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -700,11 +704,10 @@ dsa_status_t launch_merge(const DenseParams& p, int runs, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_merge_kernel<QUAD>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_merge_kernel, p);
   if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_merge_kernel launch failed: %s", cudaGetErrorString(e));
   return DSA_OK;
 }
-
 
 dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_stride, int32_t num_blocks,
                         const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
@@ -772,18 +775,21 @@ dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_st
     d.desc = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(d.ml_part) + ml_part_bytes(pairs));
   }
   d.dev_status = dev_status;
-  // Requests of two row tiles and more on average go to clusters of four CTAs,
-  // which take 256 rows at a time. Not when row tiles may not be cut: then a
-  // token's result must not depend on how long the other requests are.
-  const int quads = d.cut && static_cast<int64_t>(T) * H >= int64_t(256) * B ? num_quads(f8) : 0;
-  if (quads > 0) {
-    d.tpt = 256 / H;
-    st = launch_quads(d, f8, q, kv_cache, quads, s);
-    if (st == DSA_OK) st = launch_merge<true>(d, quads, s);
-  } else {
-    st = f8 ? launch_dense<true>(d, q, kv_cache, pairs, s) : launch_dense<false>(d, q, kv_cache, pairs, s);
-    if (st == DSA_OK && d.cut) st = launch_merge<false>(d, pairs, s);
+  // Where requests have two row tiles and more on average, a kernel that takes
+  // 256 rows at a time on four CTAs may be the faster one. The lengths, on the
+  // device, decide it: both are launched and one of them returns at once. Not
+  // when row tiles may not be cut: then a token's result must not depend on
+  // the other requests.
+  d.pairs = pairs;
+  d.quads = d.cut && static_cast<int64_t>(T) * H >= int64_t(256) * B ? num_quads(f8) : 0;
+  if (d.quads > 0) {
+    DenseParams dq = d;
+    dq.tpt = 256 / H;
+    st = launch_quads(dq, f8, q, kv_cache, d.quads, s);
+    if (st != DSA_OK) return st;
   }
+  st = f8 ? launch_dense<true>(d, q, kv_cache, pairs, s) : launch_dense<false>(d, q, kv_cache, pairs, s);
+  if (st == DSA_OK && d.cut) st = launch_merge(d, s);
   return st == DSA_OK ? check_launch(name) : st;
 }
 

@@ -36,6 +36,7 @@ struct DenseParams {
   int32_t bt_stride;
   const int32_t *seq_lens, *qsl;
   int32_t B, T, H, tpt;      // tpt: tokens per row tile
+  int32_t pairs, quads;      // runs of the pair and of the four-CTA kernel; quads = 0: the pair kernel alone
   int32_t block_size, bs64;  // bs64 = block_size / 64
   float scale_log2;
   const uint8_t* kv;  // the fp8 cache
@@ -47,7 +48,7 @@ struct DenseParams {
   // from the run before, 2 n + 1 the one it leaves to the next
   float4* o_part;   // [slot][row halves][groups of 4 TMEM columns][128 lanes]
   float2* ml_part;  // [slot][rows of a row tile]: max (log2 units), sum
-  int4* desc;       // per run: the cut row tile that starts in it (first row, rows, further parts)
+  int4* desc;       // per run: the cut row tile that starts in it (first row, rows, further parts, kernel)
   int32_t* dev_status;
 };
 
@@ -56,6 +57,7 @@ struct DenseParams {
 struct Run {
   int32_t b, tile, k0, pad;
   int64_t pos, end, per;
+  bool mine;  // this kernel works on the batch, not the other one
 };
 
 // A request's rows as work: row tile i has steps(i) = max(1, ceil(keys its
@@ -65,6 +67,8 @@ struct Request {
   int32_t c;     // position of its first new token (a length below 0 counts as 0)
   bool uneven;   // lengths that contradict each other: every tile is charged kv_len
 };
+
+constexpr int kPairTile = 1, kQuadTile = 2;  // desc's kernel
 
 __device__ __forceinline__ Request load_request(const DenseParams& p, int b) {
   Request r;
@@ -83,8 +87,8 @@ __device__ __forceinline__ Request load_request(const DenseParams& p, int b) {
 __device__ __forceinline__ int visible(const Request& r, int i) {
   return max(0, min(r.c + i + 1, r.kv_len));
 }
-__device__ __forceinline__ int steps_of(const DenseParams& p, const Request& r, int tile) {
-  const int keys = r.uneven ? r.kv_len : visible(r, min(r.q_len, (tile + 1) * p.tpt) - 1);
+__device__ __forceinline__ int steps_of(const Request& r, int tpt, int tile) {
+  const int keys = r.uneven ? r.kv_len : visible(r, min(r.q_len, (tile + 1) * tpt) - 1);
   return max(1, (keys + kTile - 1) / kTile);
 }
 // sum over i < n of floor((a i + b) / 128)
@@ -113,12 +117,12 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
     a = t;
   }
 }
-// steps of the request's row tiles before tile n
-__device__ __forceinline__ int64_t steps_before(const DenseParams& p, const Request& r, int n) {
-  if (r.uneven) return static_cast<int64_t>(n) * steps_of(p, r, 0);
+// steps of the request's first n row tiles (of n_tiles) of tpt tokens
+__device__ __forceinline__ int64_t steps_before(const Request& r, int tpt, int n_tiles, int n) {
+  if (r.uneven) return static_cast<int64_t>(n) * steps_of(r, tpt, 0);
   if (n == 0) return 0;
-  if (n < r.n_tiles) return floor_sum(n, p.tpt, static_cast<int64_t>(r.c) + p.tpt + kTile - 1);
-  return floor_sum(n - 1, p.tpt, static_cast<int64_t>(r.c) + p.tpt + kTile - 1) + steps_of(p, r, n - 1);
+  const int64_t b = static_cast<int64_t>(r.c) + tpt + kTile - 1;
+  return n < n_tiles ? floor_sum(n, tpt, b) : floor_sum(n - 1, tpt, b) + steps_of(r, tpt, n - 1);
 }
 
 // A run of steps, segment by segment (a segment: the steps of one row tile).
@@ -127,7 +131,7 @@ struct Cursor {
   int32_t b, tile, nk, k0, k1;
   int32_t left;  // steps of the run from this segment on
   __device__ __forceinline__ void cut(const DenseParams& p) {
-    nk = steps_of(p, req, tile);
+    nk = steps_of(req, p.tpt, tile);
     k1 = p.cut ? min(nk, k0 + left) : nk;
   }
   __device__ __forceinline__ bool start(const DenseParams& p, const Run* s) {
@@ -277,24 +281,39 @@ __device__ __forceinline__ Decoded decode16(const CodePair& v, int g, bool swap)
   return {decode8(swap ? c.z : c.x, swap ? c.w : c.y, sc), decode8(swap ? c.x : c.z, swap ? c.y : c.w, sc)};
 }
 
-// Run `index` of n_runs: every CTA sums the requests' steps itself. `scratch`
-// is shared memory that nothing else uses yet.
-template <int kThreads>
-__device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* scratch, int index, int n_runs) {
-  int64_t* sums = reinterpret_cast<int64_t*>(scratch);
+// Run `index` of this kernel: every CTA sums the requests' steps itself.
+// `scratch` is shared memory that nothing else uses yet.
+//
+// Where the pair and the four-CTA kernel are both launched, the lengths decide
+// here, the same in both, which of them works. A row tile of the pair kernel
+// costs about 7100 + 4400 clocks a step (128 rows, 2 SMs), one of the four-CTA
+// kernel 12300 + 2700 (256 rows, 4 SMs) and ~6000 more to begin with: fitted to
+// 16 prompts of 256 tokens (128 heads: 380 against 477 us) and chunks over long
+// contexts (1024 tokens of 16384: 3580 against 2600 us).
+template <int kThreads, bool QUAD>
+__device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* scratch, int index) {
+  int64_t* sums = reinterpret_cast<int64_t*>(scratch);  // [3][warps]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
   const bool once = p.B <= kThreads;
-  int64_t w = 0, incl = 0;
+  const int n_runs = QUAD ? p.quads : p.pairs;
+  int64_t w = 0, incl = 0, cost_pair = 0, cost_quad = 0;
   Request r = {};
-  const auto scan = [&](int b) {  // steps of request b, and their inclusive sum over the block's requests
+  const auto scan = [&](int b, bool costs) {  // steps of request b, and their inclusive sum over the block's requests
     w = 0;
+    int64_t cp = 0, cq = 0;
     if (b < p.B) {
       r = load_request(p, b);
-      if (r.uneven && r.q_len > 0 && index == 0) {
-        report(p.dev_status, DSA_DEVERR_SEQ_LEN);
+      w = steps_before(r, p.tpt, r.n_tiles, r.n_tiles);
+      if (costs) {
+        if (r.uneven && r.q_len > 0 && index == 0) report(p.dev_status, DSA_DEVERR_SEQ_LEN);
+        if (p.quads > 0 && r.q_len > 0) {
+          const int tpt = (QUAD ? 128 : 256) / p.H, n = (r.q_len + tpt - 1) / tpt;
+          const int64_t other = steps_before(r, tpt, n, n);
+          cp = QUAD ? int64_t(71) * n + 44 * other : int64_t(71) * r.n_tiles + 44 * w;
+          cq = QUAD ? int64_t(123) * r.n_tiles + 27 * w : int64_t(123) * n + 27 * other;
+        }
       }
-      w = steps_before(p, r, r.n_tiles);
     }
     incl = w;
 #pragma unroll
@@ -302,39 +321,58 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* 
       const int64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, off);
       if (lane >= off) incl += u;
     }
+    if (costs && p.quads > 0) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        cp += __shfl_xor_sync(0xFFFFFFFFu, cp, off);
+        cq += __shfl_xor_sync(0xFFFFFFFFu, cq, off);
+      }
+    }
     __syncthreads();
-    if (lane == 31) sums[warp] = incl;
+    if (lane == 31) {
+      sums[warp] = incl;
+      sums[kWarps + warp] = cp;
+      sums[2 * kWarps + warp] = cq;
+    }
     __syncthreads();
     int64_t all = 0;
     for (int i = 0; i < kWarps; ++i) {
       if (i < warp) incl += sums[i];
       all += sums[i];
+      if (costs && p.quads > 0) {
+        cost_pair += sums[kWarps + i];
+        cost_quad += sums[2 * kWarps + i];
+      }
     }
     return all;
   };
   int64_t total = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) total += scan(b0 + tid);
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) total += scan(b0 + tid, true);
+  const bool mine =
+      p.quads == 0 || (cost_quad * p.pairs + int64_t(60) * p.pairs * p.quads < cost_pair * p.quads) == QUAD;
+  if (!mine) total = 0;
   int64_t per = (total + n_runs - 1) / n_runs;
   if (p.cut) per = max(per, int64_t(kMinRun));
   const int64_t u0 = per * index, u1 = min(u0 + per, total);
   if (tid == 0) {
     s->per = per;
+    s->mine = mine;
     s->pos = s->end = 0;
   }
   __syncthreads();
   if (u0 < u1) {
     int64_t base = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-      const int64_t all = once ? total : scan(b0 + tid);
+      const int64_t all = once ? total : scan(b0 + tid, false);
       const int64_t from = base + incl - w;
       if (w > 0 && from <= u0 && u0 < from + w) {
         const int64_t u = u0 - from;
         int lo = 0, hi = r.n_tiles - 1;  // the last row tile that starts at or before u
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (steps_before(p, r, mid) <= u) lo = mid; else hi = mid - 1;
+          if (steps_before(r, p.tpt, r.n_tiles, mid) <= u) lo = mid; else hi = mid - 1;
         }
-        const int64_t at = steps_before(p, r, lo);
+        const int64_t at = steps_before(r, p.tpt, r.n_tiles, lo);
         s->b = b0 + tid;
         s->tile = lo;
         s->k0 = static_cast<int32_t>(u - at);
@@ -342,7 +380,7 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* 
         s->end = u1;
         if (!p.cut && u > at) {  // the row tile belongs to the run it starts in: begin with the next
           s->k0 = 0;
-          s->pos = from + steps_before(p, r, lo + 1);
+          s->pos = from + steps_before(r, p.tpt, r.n_tiles, lo + 1);
           if (lo + 1 < r.n_tiles) {
             s->tile = lo + 1;
           } else if (s->pos < u1) {

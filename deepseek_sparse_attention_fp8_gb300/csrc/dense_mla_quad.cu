@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_ctarank()), a = rank & 1;  // a: row half
   const bool values = rank >= 2;
-  const int quad = blockIdx.x >> 2, n_quads = gridDim.x >> 2;
+  const int quad = blockIdx.x >> 2;
 
   if (smem_u32(smem) & 1023u) {  // the tiles need it (without static arrays the dynamic part starts there)
     if (tid == 0) report(p.dev_status, DSA_DEVERR_TIMEOUT);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
   tc_fence_after();
   const uint32_t tmem = s->tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_run<kThreadsOf<F8>>(p, &s->run, smem, quad, n_quads);
+  plan_run<kThreadsOf<F8>, true>(p, &s->run, smem, quad);
 
   const auto abort_now = [&] {
     s->abort = 1;
@@ -707,14 +707,16 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
           const int64_t at = s->run.end - c.left;
           const int last = static_cast<int>((at + c.nk - 1) / s->run.per);
           const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt) - c.tile * p.tpt) * p.H;
-          p.desc[quad] = make_int4((c.req.q0 + c.tile * p.tpt) * p.H, rows, last - quad, 0);
+          p.desc[quad] = make_int4((c.req.q0 + c.tile * p.tpt) * p.H, rows, last - quad, kQuadTile);
         }
       }
       tc_fence_before();
     }
-    if (p.cut && rank == 2 && tid == 0) {
-      // nothing to join: no row tile that starts in this run goes on behind it
+    if (rank == 2 && tid == 0 && s->run.mine) {
+      // nothing to join: no row tile that starts in this run goes on behind it;
+      // and the pair kernel's runs beyond leave nothing
       if (!ok || s->run.pos >= s->run.end || c.k0 > 0 || c.k1 == c.nk) p.desc[quad] = make_int4(0, 0, 0, 0);
+      for (int i = quad + p.quads; i < p.pairs; i += p.quads) p.desc[i] = make_int4(0, 0, 0, 0);
     }
   }
 

@@ -68,6 +68,86 @@ def test_dense_attention(name, fp8, splits):
     check(make_dense_case(lens, q_lens, H, fp8=fp8, block=block, seed=len(name)), splits)
 
 
+# several row tiles a request over long contexts: the four-CTA kernel's
+LONG_CASES = {
+    "two_tokens": ([9000, 12000, 3000, 7000], [2, 2, 2, 2], 128, 64),
+    "odd_tokens": ([5000, 4097], [3, 5], 128, 64),
+    "chunks": ([2500, 900], [40, 33], 128, 192),
+    "heads100": ([6000, 2049], [7, 3], 100, 64),
+    "heads40": ([4000, 8191, 5000], [13, 6, 20], 40, 128),
+    "heads16": ([6100, 3000], [150, 17], 16, 64),
+    "heads3": ([9000], [300], 3, 64),
+    "one_cut_tile": ([30000], [2], 128, 256),
+    "long_and_short": ([20000, 1, 64, 130, 9000], [20, 1, 2, 1, 9], 64, 64),
+    "idle_requests": ([0, 8000, 5, 7000], [0, 6, 0, 4], 128, 64),
+}
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("name", sorted(LONG_CASES))
+def test_long_chunks(name, fp8):
+    lens, q_lens, H, block = LONG_CASES[name]
+    check(make_dense_case(lens, q_lens, H, fp8=fp8, block=block, seed=len(name)))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_chunks_with_bad_blocks_and_lengths(fp8):
+    """Masked blocks, a request with fewer keys than tokens, padded rows, and
+    blocks further apart than their rows."""
+    c = make_dense_case([6000, 3, 7000], [6, 5, 4], 128, fp8=fp8, seed=31, pad_tokens=3, extra_rows=8, extra_cols=2)
+    for b, j, v in ((0, 1, 10 ** 6), (0, 93, -5), (2, 40, int(c["cache"].shape[0])), (2, 109, -1)):
+        c["table"][b, j] = v
+    out, lse = check(c, status=api.DSA_DEVERR_BLOCK_OOB | api.DSA_DEVERR_SEQ_LEN,
+                     blocked={(0, 1), (0, 93), (2, 40), (2, 109)})
+    assert torch.isnan(out[15:]).all() and torch.isnan(lse[15:]).all()
+    assert (out[6:8] == 0).all() and torch.isneginf(lse[6:8]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("q_std", [0.0, 300.0])
+def test_long_chunks_score_ranges(fp8, q_std):
+    check(make_dense_case([7000, 5000], [4, 6], 128, fp8=fp8, q_std=q_std, seed=32))
+
+
+def test_long_chunks_rising_scores():
+    """Scores that grow along the keys rescale the outputs step after step."""
+    c = make_dense_case([6000], [4], 128, seed=33)
+    q = c["q"][0, 0].float()
+    n = (torch.arange(6000, device="cuda", dtype=torch.float32) / 50.0)[:, None]
+    rows = (q / q.pow(2).sum() / SCALE)[None, :] * n + 0.05 * torch.randn((6000, 576), device="cuda")
+    pages = torch.zeros((94, 64, 576), device="cuda")
+    pages.view(-1, 576)[:6000] = rows
+    c["cache"][c["table"][0].long()] = pages.to(torch.bfloat16)
+    c["q"][:] = c["q"][0, 0]
+    check(c)
+
+
+def test_captured_graph_follows_lengths_between_the_kernels():
+    """Long and short contexts, chunks and none, in replays of one graph."""
+    c = make_dense_case([9000, 7000], [8, 8], 128, seed=34)
+    ws = torch.full((api.dense_mla_workspace_size(16, 128, DV, 0),), 0xFF, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty((16, 128, DV), dtype=torch.bfloat16, device="cuda"), torch.empty((16, 128), device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (c["q"], c["cache"], c["table"], c["seq"], c["qsl"], SCALE, DV, out)
+    api.dense_mla_attention(*args, lse=lse, workspace=ws, dev_status=st)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        api.dense_mla_attention(*args, lse=lse, workspace=ws, dev_status=st)
+    for lens, q_lens in (([9000, 7000], [8, 8]), ([60, 100], [8, 8]), ([8, 0], [0, 0]), ([8999, 6000], [16, 0]),
+                         ([9000, 300], [1, 15])):
+        c["seq"].copy_(torch.tensor(lens, dtype=torch.int32))
+        c["qsl"].copy_(torch.tensor(np.concatenate([[0], np.cumsum(q_lens)]), dtype=torch.int32))
+        out.fill_(float("nan"))
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        n = sum(q_lens)
+        assert int(st.item()) == 0 and torch.isnan(out[n:]).all()
+        if n:
+            check_dense(out[:n], lse[:n], dense_reference(dict(c, lens=lens, q_lens=q_lens, T=n)))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_block_stride_and_wide_table(fp8):
     check(make_dense_case([300, 70, 129], [3, 1, 2], 16, fp8=fp8, extra_rows=8, extra_cols=5, seed=3))
