@@ -3,14 +3,18 @@
 // of free blocks (another prefix sum, of ceil((ctx+new)/bs) - ceil(ctx/bs)),
 // and per token its request, position and cache slot.
 //
-// One cluster of CTAs (of one CTA for a small batch), so that the queue's head
-// can be read by all and advanced in place behind a cluster barrier. The
-// requests are taken in chunks of one per thread: every CTA makes a chunk's
-// two prefix sums (block scans with a carry) itself, then the cluster's
+// The requests are taken in chunks of one per thread: every CTA makes a chunk's
+// two prefix sums (one block scan of both, with a carry) itself, then all
 // threads share the chunk's tokens, four in a row each: one binary search in
 // shared memory, and full 16-byte stores. A token at the first position of a
-// new block stores the block in the table, so no thread walks a long
-// request's blocks alone.
+// new block stores the block in the table, so no thread walks a long request's
+// blocks alone. Latency bounds it: a launch, the lengths, the free ids, the
+// stores. When the queue's head is advanced in place the CTAs form one cluster,
+// whose barrier keeps the head until all have read it; else there are as many
+// as the tokens fill. (512 requests, 131000 tokens: one CTA 141 us, a cluster
+// of 8 18 us.)
+#include <algorithm>
+
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -18,7 +22,7 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kCluster = 8, kOneCta = 4096;
+constexpr int kCluster = 8;
 
 struct BatchParams {
   const int32_t *ctx, *add, *free_blocks, *free_head;
@@ -31,31 +35,40 @@ struct BatchParams {
   int32_t* dev_status;
 };
 
-// Inclusive scan over the block; *total is the block's sum.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+// Inclusive scans of two values over the block; total: the block's sums.
+__device__ __forceinline__ longlong2 block_scan(longlong2 v, longlong2* warp_sums, longlong2* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const auto scan = [&](longlong2 x) {
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, off);
-    if (lane >= off) v += u;
-  }
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t a = __shfl_up_sync(0xFFFFFFFFu, x.x, off), b = __shfl_up_sync(0xFFFFFFFFu, x.y, off);
+      if (lane >= off) {
+        x.x += a;
+        x.y += b;
+      }
+    }
+    return x;
+  };
+  v = scan(v);
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  int64_t before = 0, sum = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int64_t s = warp_sums[w];
-    if (w < warp) before += s;
-    sum += s;
+  static_assert(kThreads == 1024, "a lane per warp");
+  const longlong2 s = scan(warp_sums[lane]);
+  total->x = __shfl_sync(0xFFFFFFFFu, s.x, 31);
+  total->y = __shfl_sync(0xFFFFFFFFu, s.y, 31);
+  const int64_t bx = __shfl_sync(0xFFFFFFFFu, s.x, (warp - 1) & 31), by = __shfl_sync(0xFFFFFFFFu, s.y, (warp - 1) & 31);
+  if (warp > 0) {
+    v.x += bx;
+    v.y += by;
   }
-  *total = sum;
   __syncthreads();  // the sums may be overwritten
-  return v + before;
+  return v;
 }
 
 __global__ void __launch_bounds__(kThreads) build_batch_kernel(const __grid_constant__ BatchParams p) {
-  __shared__ int64_t warp_sums[kThreads / 32];
+  __shared__ longlong2 warp_sums[kThreads / 32];
   __shared__ int32_t s_start[kThreads + 1], s_ctx[kThreads], s_take[kThreads];
-  const int tid = threadIdx.x, rank = blockIdx.x;  // the grid is one cluster
+  const int tid = threadIdx.x, rank = blockIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
   uint32_t err = 0;
   const int64_t head = p.free_blocks != nullptr ? *p.free_head : 0;
@@ -73,18 +86,25 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const __grid_cons
         a = 0;
       }
     }
-    int64_t sum;
-    const int64_t last = tokens + block_scan(a, warp_sums, &sum);
-    const int64_t cap = p.max_tokens;
-    const int64_t start = min(last - a, cap);
-    if (last > cap) err |= a > 0 ? DSA_DEVERR_SEQ_LEN : 0u;
-    a = min(last, cap) - start;
-    const int64_t held = (c + p.block_size - 1) / p.block_size;
-    int64_t take = 0;
-    if (tid < n && p.free_blocks != nullptr)
-      take = max(int64_t(0), min((c + a + p.block_size - 1) / p.block_size, int64_t(p.bt_stride)) - held);
-    int64_t sum_take;
-    const int64_t take_end = taken + block_scan(take, warp_sums, &sum_take);
+    const int64_t cap = p.max_tokens, held = (c + p.block_size - 1) / p.block_size;
+    const auto blocks_taken = [&](int64_t add) {
+      return tid < n && p.free_blocks != nullptr
+                 ? max(int64_t(0), min((c + add + p.block_size - 1) / p.block_size, int64_t(p.bt_stride)) - held)
+                 : int64_t(0);
+    };
+    int64_t take = blocks_taken(a);
+    longlong2 sum;
+    longlong2 upto = block_scan(make_longlong2(a, take), warp_sums, &sum);
+    const int64_t last = tokens + upto.x, start = min(last - a, cap);
+    if (tokens + sum.x > cap) {  // the buffers are full: tokens are dropped, and their blocks not taken
+      if (last > cap && a > 0) err |= DSA_DEVERR_SEQ_LEN;
+      a = min(last, cap) - start;
+      take = blocks_taken(a);
+      longlong2 less;
+      upto = block_scan(make_longlong2(a, take), warp_sums, &less);
+      sum.y = less.y;
+    }
+    const int64_t take_end = taken + upto.y;
     if (tid < n) {
       s_start[tid] = static_cast<int32_t>(start);
       s_ctx[tid] = static_cast<int32_t>(c);
@@ -98,8 +118,8 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const __grid_cons
         if (b == p.B - 1) p.qsl[p.B] = static_cast<int32_t>(start + a);
       }
     }
-    tokens += sum;
-    taken += sum_take;
+    tokens += sum.x;
+    taken += sum.y;
     __syncthreads();
     const int first = s_start[0], end = s_start[n];
     // four tokens from a multiple of 4 on; the chunk may begin and end inside
@@ -171,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const __grid_cons
     p.positions[t] = 0;
     p.slot_map[t] = -1;
   }
-  if (gridDim.x > 1) ptx::cluster_sync_all();  // every CTA has read the head
+  if (p.free_head == p.free_head_out && gridDim.x > 1) ptx::cluster_sync_all();  // every CTA has read the head
   if (rank == 0 && tid == 0 && p.free_blocks != nullptr)
     *p.free_head_out = static_cast<int32_t>(head_ok ? min(head + taken, int64_t(p.num_free)) : head);
   if (err) report(p.dev_status, err);
@@ -222,10 +242,10 @@ extern "C" dsa_status_t dsa_build_batch(const int32_t* ctx_lens, const int32_t* 
   p.slot_map = slot_map;
   p.dev_status = dev_status;
   p.vec = aligned16(token_req) && aligned16(positions) && aligned16(slot_map);
-  // a CTA serves up to kOneCta tokens about as fast as a cluster does, whose
-  // launch and barrier cost more
+  const bool in_place = free_blocks && free_head == free_head_out;
+  const int ctas = std::min((max_tokens + kThreads * 4 - 1) / (kThreads * 4), in_place ? kCluster : num_sms());
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(max_tokens <= kOneCta ? 1 : kCluster);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(ctas, 1)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -234,7 +254,7 @@ extern "C" dsa_status_t dsa_build_batch(const int32_t* ctx_lens, const int32_t* 
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = in_place ? 1 : 0;
   cudaError_t e = cudaLaunchKernelEx(&cfg, build_batch_kernel, p);
   if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "build_batch_kernel launch failed: %s", cudaGetErrorString(e));
   return check_launch("build_batch_kernel");

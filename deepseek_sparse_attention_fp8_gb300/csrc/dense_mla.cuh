@@ -35,8 +35,8 @@ struct DenseParams {
   const int32_t* block_table;
   int32_t bt_stride;
   const int32_t *seq_lens, *qsl;
-  int32_t B, T, H, tpt;      // tpt: tokens per row tile
-  int32_t pairs, quads;      // runs of the pair and of the four-CTA kernel; quads = 0: the pair kernel alone
+  int32_t B, T, H, tpt[2];   // tokens per row tile of a pair, of a quad
+  int32_t pairs, quads;      // pairs and quads of CTAs launched; quads = 0: pairs only
   int32_t block_size, bs64;  // bs64 = block_size / 64
   float scale_log2;
   const uint8_t* kv;  // the fp8 cache
@@ -48,17 +48,19 @@ struct DenseParams {
   // from the run before, 2 n + 1 the one it leaves to the next
   float4* o_part;   // [slot][row halves][groups of 4 TMEM columns][128 lanes]
   float2* ml_part;  // [slot][rows of a row tile]: max (log2 units), sum
-  int4* desc;       // per run: the cut row tile that starts in it (first row, rows, further parts, kernel)
+  int4* desc;       // per run: the cut row tile that starts in it (first row, rows, further parts, quad)
   int32_t* dev_status;
 };
 
 // The run of a group of CTAs: its first request, row tile and step, and its
-// steps [pos, end) of all; per: steps of every run.
+// steps [pos, end) of all; per: steps of every run. At the end of shared memory.
 struct Run {
-  int32_t b, tile, k0, pad;
+  int32_t b, tile, k0, index;
   int64_t pos, end, per;
-  bool mine;  // this kernel works on the batch, not the other one
+  bool quad;  // the batch is worked on by quads
 };
+constexpr int kSmTotal = 232448, kSmRun = kSmTotal - 64;
+static_assert(sizeof(Run) <= 64, "run block too large");
 
 // A request's rows as work: row tile i has steps(i) = max(1, ceil(keys its
 // last token sees / 128)).
@@ -68,15 +70,13 @@ struct Request {
   bool uneven;   // lengths that contradict each other: every tile is charged kv_len
 };
 
-constexpr int kPairTile = 1, kQuadTile = 2;  // desc's kernel
-
-__device__ __forceinline__ Request load_request(const DenseParams& p, int b) {
+__device__ __forceinline__ Request load_request(const DenseParams& p, int tpt, int b) {
   Request r;
   const int q0 = min(max(__ldg(p.qsl + b), 0), p.T), q1 = min(max(__ldg(p.qsl + b + 1), 0), p.T);
   const int64_t sl = __ldg(p.seq_lens + b), cap = static_cast<int64_t>(p.bt_stride) * p.block_size;
   r.q0 = q0;
   r.q_len = max(q1 - q0, 0);
-  r.n_tiles = (r.q_len + p.tpt - 1) / p.tpt;
+  r.n_tiles = (r.q_len + tpt - 1) / tpt;
   // at most 2^31 - 256, so that sums of a few steps stay within 31 bits
   r.kv_len = static_cast<int32_t>(max(int64_t(0), min(min(sl, cap), int64_t(0x7FFFFF00))));
   r.c = static_cast<int32_t>(max(sl, int64_t(0))) - r.q_len;
@@ -126,12 +126,13 @@ __device__ __forceinline__ int64_t steps_before(const Request& r, int tpt, int n
 }
 
 // A run of steps, segment by segment (a segment: the steps of one row tile).
+template <bool QUAD>
 struct Cursor {
   Request req;
   int32_t b, tile, nk, k0, k1;
   int32_t left;  // steps of the run from this segment on
   __device__ __forceinline__ void cut(const DenseParams& p) {
-    nk = steps_of(req, p.tpt, tile);
+    nk = steps_of(req, p.tpt[QUAD], tile);
     k1 = p.cut ? min(nk, k0 + left) : nk;
   }
   __device__ __forceinline__ bool start(const DenseParams& p, const Run* s) {
@@ -140,7 +141,7 @@ struct Cursor {
     k0 = k1 = nk = s->k0;
     left = static_cast<int32_t>(s->end - s->pos);
     if (left <= 0) return false;
-    req = load_request(p, b);
+    req = load_request(p, p.tpt[QUAD], b);
     cut(p);
     return true;
   }
@@ -152,7 +153,7 @@ struct Cursor {
       tile = 0;
       do {
         if (++b >= p.B) return false;
-        req = load_request(p, b);
+        req = load_request(p, p.tpt[QUAD], b);
       } while (req.n_tiles == 0);
     }
     cut(p);
@@ -170,25 +171,29 @@ struct Rows {
 // so that no step waits for the table. Called by whole warps.
 struct Units {
   int32_t base, row, ahead;
-  __device__ __forceinline__ int32_t entry(const DenseParams& p, const Cursor& c, int unit) const {
+  template <class C>
+  __device__ __forceinline__ int32_t entry(const DenseParams& p, const C& c, int unit) const {
     const int64_t key = static_cast<int64_t>(unit) * 64;
     return key < c.req.kv_len ? __ldg(p.block_table + static_cast<int64_t>(c.b) * p.bt_stride + unit / p.bs64) : 0;
   }
-  __device__ __forceinline__ int32_t first_row(const DenseParams& p, const Cursor& c, int32_t blk, int unit, bool rep) const {
+  template <class C>
+  __device__ __forceinline__ int32_t first_row(const DenseParams& p, const C& c, int32_t blk, int unit, bool rep) const {
     if (blk < 0 || blk >= p.num_blocks) {
       if (rep && static_cast<int64_t>(unit) * 64 < c.req.kv_len) report(p.dev_status, DSA_DEVERR_BLOCK_OOB);
       return -1;
     }
     return blk * p.rows_per_block + (unit % p.bs64) * 64;
   }
-  __device__ __forceinline__ void start(const DenseParams& p, const Cursor& c, int lane, bool rep) {
+  template <class C>
+  __device__ __forceinline__ void start(const DenseParams& p, const C& c, int lane, bool rep) {
     base = 2 * c.k0;
     row = entry(p, c, base + lane);
     ahead = entry(p, c, base + 32 + lane);
     row = first_row(p, c, row, base + lane, rep);
   }
   // units are asked for in ascending order, at most 32 behind the last
-  __device__ __forceinline__ Rows get(const DenseParams& p, const Cursor& c, int unit, int lane, bool rep) {
+  template <class C>
+  __device__ __forceinline__ Rows get(const DenseParams& p, const C& c, int unit, int lane, bool rep) {
     if (unit >= base + 32) {
       base += 32;
       row = first_row(p, c, ahead, base + lane, rep);
@@ -281,39 +286,59 @@ __device__ __forceinline__ Decoded decode16(const CodePair& v, int g, bool swap)
   return {decode8(swap ? c.z : c.x, swap ? c.w : c.y, sc), decode8(swap ? c.x : c.z, swap ? c.y : c.w, sc)};
 }
 
-// Run `index` of this kernel: every CTA sums the requests' steps itself.
+// The run of this pair or quad: every CTA sums the requests' steps itself.
 // `scratch` is shared memory that nothing else uses yet.
 //
-// Where the pair and the four-CTA kernel are both launched, the lengths decide
-// here, the same in both, which of them works. A row tile of the pair kernel
-// costs about 7100 + 4400 clocks a step (128 rows, 2 SMs), one of the four-CTA
-// kernel 12300 + 2700 (256 rows, 4 SMs) and ~6000 more to begin with: fitted to
-// 16 prompts of 256 tokens (128 heads: 380 against 477 us) and chunks over long
-// contexts (1024 tokens of 16384: 3580 against 2600 us).
-template <int kThreads, bool QUAD>
-__device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* scratch, int index) {
-  int64_t* sums = reinterpret_cast<int64_t*>(scratch);  // [3][warps]
+// QUADS: in clusters of four CTAs the lengths, which only the device knows,
+// decide here whether each cluster works as a quad or as two pairs. A row tile
+// costs a pair about 7100 + 4400 clocks a step (128 rows, 2 SMs), a quad 12300
+// + 2700 (256 rows, 4 SMs) and ~12000 more to begin with: fitted to 16 prompts
+// of 256 tokens (128 heads: 380 us on pairs, 477 on quads) and to 1024 tokens
+// over a context of 16384 (3580 and 2600 us).
+template <int kThreads, bool QUADS>
+__device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* scratch) {
+  int64_t* sums = reinterpret_cast<int64_t*>(scratch);  // [4][warps]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
   const bool once = p.B <= kThreads;
-  const int n_runs = QUAD ? p.quads : p.pairs;
-  int64_t w = 0, incl = 0, cost_pair = 0, cost_quad = 0;
-  Request r = {};
-  const auto scan = [&](int b, bool costs) {  // steps of request b, and their inclusive sum over the block's requests
-    w = 0;
-    int64_t cp = 0, cq = 0;
-    if (b < p.B) {
-      r = load_request(p, b);
-      w = steps_before(r, p.tpt, r.n_tiles, r.n_tiles);
-      if (costs) {
-        if (r.uneven && r.q_len > 0 && index == 0) report(p.dev_status, DSA_DEVERR_SEQ_LEN);
-        if (p.quads > 0 && r.q_len > 0) {
-          const int tpt = (QUAD ? 128 : 256) / p.H, n = (r.q_len + tpt - 1) / tpt;
-          const int64_t other = steps_before(r, tpt, n, n);
-          cp = QUAD ? int64_t(71) * n + 44 * other : int64_t(71) * r.n_tiles + 44 * w;
-          cq = QUAD ? int64_t(123) * r.n_tiles + 27 * w : int64_t(123) * n + 27 * other;
-        }
+  int64_t total = 0;
+  bool quad = false;
+  if constexpr (QUADS) {
+    int64_t tiles[2] = {0, 0}, steps[2] = {0, 0};
+    for (int b = tid; b < p.B; b += kThreads) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const Request r = load_request(p, p.tpt[q], b);
+        tiles[q] += r.n_tiles;
+        steps[q] += steps_before(r, p.tpt[q], r.n_tiles, r.n_tiles);
       }
+    }
+    int64_t cost[2] = {71 * tiles[0] + 44 * steps[0], 123 * tiles[1] + 27 * steps[1]};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) cost[q] += __shfl_xor_sync(0xFFFFFFFFu, cost[q], off);
+      if (lane == 0) sums[q * kWarps + warp] = cost[q];
+    }
+    __syncthreads();
+    cost[0] = cost[1] = 0;
+    for (int i = 0; i < kWarps; ++i) {
+      cost[0] += sums[i];
+      cost[1] += sums[kWarps + i];
+    }
+    quad = cost[1] * p.pairs + int64_t(120) * p.pairs * p.quads < cost[0] * p.quads;
+    __syncthreads();
+  }
+  const int tpt = p.tpt[quad];
+  const int index = quad ? blockIdx.x >> 2 : blockIdx.x >> 1, n_runs = quad ? p.quads : p.pairs;
+  int64_t w = 0, incl = 0;
+  Request r = {};
+  const auto scan = [&](int b, bool first) {  // steps of request b, and their inclusive sum over the block's requests
+    w = 0;
+    if (b < p.B) {
+      r = load_request(p, tpt, b);
+      if (first && r.uneven && r.q_len > 0 && index == 0) report(p.dev_status, DSA_DEVERR_SEQ_LEN);
+      w = steps_before(r, tpt, r.n_tiles, r.n_tiles);
     }
     incl = w;
 #pragma unroll
@@ -321,42 +346,24 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* 
       const int64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, off);
       if (lane >= off) incl += u;
     }
-    if (costs && p.quads > 0) {
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        cp += __shfl_xor_sync(0xFFFFFFFFu, cp, off);
-        cq += __shfl_xor_sync(0xFFFFFFFFu, cq, off);
-      }
-    }
     __syncthreads();
-    if (lane == 31) {
-      sums[warp] = incl;
-      sums[kWarps + warp] = cp;
-      sums[2 * kWarps + warp] = cq;
-    }
+    if (lane == 31) sums[warp] = incl;
     __syncthreads();
     int64_t all = 0;
     for (int i = 0; i < kWarps; ++i) {
       if (i < warp) incl += sums[i];
       all += sums[i];
-      if (costs && p.quads > 0) {
-        cost_pair += sums[kWarps + i];
-        cost_quad += sums[2 * kWarps + i];
-      }
     }
     return all;
   };
-  int64_t total = 0;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) total += scan(b0 + tid, true);
-  const bool mine =
-      p.quads == 0 || (cost_quad * p.pairs + int64_t(60) * p.pairs * p.quads < cost_pair * p.quads) == QUAD;
-  if (!mine) total = 0;
   int64_t per = (total + n_runs - 1) / n_runs;
   if (p.cut) per = max(per, int64_t(kMinRun));
   const int64_t u0 = per * index, u1 = min(u0 + per, total);
   if (tid == 0) {
+    s->index = index;
+    s->quad = quad;
     s->per = per;
-    s->mine = mine;
     s->pos = s->end = 0;
   }
   __syncthreads();
@@ -370,9 +377,9 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* 
         int lo = 0, hi = r.n_tiles - 1;  // the last row tile that starts at or before u
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (steps_before(r, p.tpt, r.n_tiles, mid) <= u) lo = mid; else hi = mid - 1;
+          if (steps_before(r, tpt, r.n_tiles, mid) <= u) lo = mid; else hi = mid - 1;
         }
-        const int64_t at = steps_before(r, p.tpt, r.n_tiles, lo);
+        const int64_t at = steps_before(r, tpt, r.n_tiles, lo);
         s->b = b0 + tid;
         s->tile = lo;
         s->k0 = static_cast<int32_t>(u - at);
@@ -380,12 +387,12 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* 
         s->end = u1;
         if (!p.cut && u > at) {  // the row tile belongs to the run it starts in: begin with the next
           s->k0 = 0;
-          s->pos = from + steps_before(r, p.tpt, r.n_tiles, lo + 1);
+          s->pos = from + steps_before(r, tpt, r.n_tiles, lo + 1);
           if (lo + 1 < r.n_tiles) {
             s->tile = lo + 1;
           } else if (s->pos < u1) {
             int b = b0 + tid;
-            do ++b; while (load_request(p, b).n_tiles == 0);
+            do ++b; while (load_request(p, tpt, b).n_tiles == 0);
             s->b = b;
             s->tile = 0;
           }
@@ -398,10 +405,36 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* 
   __syncthreads();
 }
 
+// Tensor maps of a call: q in boxes of q_rows x 64 x q_blocks dims; the cache
+// as 9 blocks of 64 dims a row, block-major boxes (keys: 64 keys x 128 dims;
+// rope: 64 keys x 64; row: one row x 64, for gathers). fp8: the cache's maps
+// cover the rope dims only (128 bytes from byte 528 of a row).
+struct Maps {
+  CUtensorMap q, keys, rope, row;
+};
+inline dsa_status_t make_maps(Maps* m, const DenseParams& p, bool f8, const void* q, const void* kv, uint32_t q_rows,
+                              uint32_t q_blocks) {
+  const void* base = f8 ? static_cast<const uint8_t*>(kv) + kDv + 16 : kv;
+  const uint64_t rows = static_cast<uint64_t>(p.total_rows), blocks = f8 ? 1 : 9;
+  const uint64_t q_strides[2] = {kDk * 2, 128}, strides[2] = {f8 ? uint64_t(kF8Row) : uint64_t(kDk * 2), 128};
+  const uint64_t q_dims[3] = {64, static_cast<uint64_t>(p.T) * p.H, 9}, dims[3] = {64, rows, blocks};
+  const uint64_t row_dims[2] = {64 * blocks, rows};
+  const uint32_t q_box[3] = {64, q_rows, q_blocks}, keys_box[3] = {64, 64, f8 ? 1u : 2u}, rope_box[3] = {64, 64, 1};
+  const uint32_t row_box[2] = {64, 1};
+  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  dsa_status_t st;
+  if ((st = make_tmap(&m->q, bf16, 3, q, q_dims, q_strides, q_box, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&m->keys, bf16, 3, base, dims, strides, keys_box, sw)) != DSA_OK) return st;
+  if ((st = make_tmap(&m->rope, bf16, 3, base, dims, strides, rope_box, sw)) != DSA_OK) return st;
+  return make_tmap(&m->row, bf16, 2, base, row_dims, strides, row_box, sw);
+}
+
 // Number of 4-CTA clusters the current device runs at once, 0 when it cannot.
 int num_quads(bool f8);
-// Enqueues the four-CTA kernel (p.tpt tokens per row tile of 256 rows).
-dsa_status_t launch_quads(const DenseParams& p, bool f8, const void* q, const void* kv, int quads, cudaStream_t s);
+// Enqueues the kernel of clusters of four CTAs, p.quads of them, which work as
+// quads or as 2 p.quads = p.pairs pairs.
+dsa_status_t launch_quads(const DenseParams& p, bool f8, const void* q, const void* kv, cudaStream_t s);
 
 }  // namespace dense
 }  // namespace dsa

@@ -17,7 +17,7 @@
 // takes in, against 2300 and 2050 of MMA, for twice the rows of a pair's step.
 #include <algorithm>
 
-#include "dense_mla.cuh"
+#include "dense_mla_pair.cuh"
 
 namespace dsa {
 namespace dense {
@@ -40,8 +40,8 @@ constexpr uint32_t kTmemCols = 512, kColS = 0, kColQ = 256;  // CTAs 0, 1: S 2 x
 constexpr int kRing = 10;
 constexpr int kSmRopeK = kRing * kSlot, kSmRopeQ = kSmRopeK + 2 * 8192, kSmPOut = kSmRopeQ + 16384, kSmRed = kSmPOut + 32768, kSmAlphaOut = kSmRed + 2048;
 constexpr int kSmP = kRing * kSlot, kSmAlpha = kSmP + 2 * 32768, kSmMl = kSmAlpha + 2 * 128 * 4;
-constexpr int kSmBar = kSmAlphaOut + 512, kSmTotal = kSmBar + 512;
-static_assert(kSmTotal <= 232448 && kSmMl + 1024 <= kSmBar, "shared memory");
+constexpr int kSmBar = kSmAlphaOut + 512;
+static_assert(kSmBar + 448 <= kSmRun && kSmMl + 1024 <= kSmBar, "shared memory");
 
 struct Bars {  // at the same offset in every CTA
   uint64_t full[kRing], empty[kRing];  // ring slots; full: of both CTAs of a pair, the even one's barrier
@@ -61,17 +61,9 @@ struct Bars {  // at the same offset in every CTA
   uint64_t pv_done[2];
   uint32_t tmem;
   volatile int abort;
-  Run run;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block too large");
+static_assert(sizeof(Bars) <= 448, "barrier block too large");
 
-__device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t ctas) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(ctas)
-      : "memory");
-}
 __device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc_lo, uint32_t bdesc_hi,
                                                  uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -113,23 +105,16 @@ struct Ring {
   }
 };
 
+// Works on this quad's run, and ends with a cluster barrier.
 template <bool F8>
-__global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const __grid_constant__ DenseParams p,
-                                                                     const __grid_constant__ CUtensorMap qmap,
-                                                                     const __grid_constant__ CUtensorMap kvmap,
-                                                                     const __grid_constant__ CUtensorMap ropemap,
-                                                                     const __grid_constant__ CUtensorMap rowmap) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+__device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps, uint8_t* smem) {
   Bars* s = reinterpret_cast<Bars*>(smem + kSmBar);
+  const Run* run = reinterpret_cast<const Run*>(smem + kSmRun);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_ctarank()), a = rank & 1;  // a: row half
   const bool values = rank >= 2;
-  const int quad = blockIdx.x >> 2;
+  const int quad = run->index;
 
-  if (smem_u32(smem) & 1023u) {  // the tiles need it (without static arrays the dynamic part starts there)
-    if (tid == 0) report(p.dev_status, DSA_DEVERR_TIMEOUT);
-    return;
-  }
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&s->full[i], F8 ? 2 * kDecodeWarps : 1);
@@ -161,17 +146,15 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
     tmem_relinquish_pair();
   }
   if (tid == kLoadWarp * 32) {
-    prefetch_tmap(&qmap);
-    prefetch_tmap(&kvmap);
-    prefetch_tmap(&ropemap);
-    prefetch_tmap(&rowmap);
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.keys);
+    prefetch_tmap(&maps.rope);
+    prefetch_tmap(&maps.row);
   }
   tc_fence_before();
   cluster_sync_all();  // all CTAs' barriers exist
   tc_fence_after();
   const uint32_t tmem = s->tmem;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_run<kThreadsOf<F8>, true>(p, &s->run, smem, quad);
 
   const auto abort_now = [&] {
     s->abort = 1;
@@ -180,7 +163,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
   // a barrier's or buffer's address in another CTA
   const auto in_cta = [&](const void* x, int cta) { return mapa_shared(smem_u32(x), static_cast<uint32_t>(cta)); };
   const int even = rank & ~1;
-  Cursor c;
+  Cursor<true> c;
 
   if (warp == kLoadWarp && !values) {
     // ---------------- q of each row tile, then the own keys of its steps
@@ -192,20 +175,20 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
       if (ring.turn > 0 && !warp_wait(&s->empty[ring.slot], (ring.turn - 1) & 1)) ok = false;
       return ok;
     };
-    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
-      const int row0 = (c.req.q0 + c.tile * p.tpt) * p.H + 128 * a;
+    for (bool more = c.start(p, run); more && ok; more = c.next(p), ++seg) {
+      const int row0 = (c.req.q0 + c.tile * p.tpt[1]) * p.H + 128 * a;
       if (seg > 0 && !warp_wait(&s->q_rope_free, (seg - 1) & 1)) {
         ok = false;
         break;
       }
       if (lane == 0) {
         mbar_arrive_expect_tx(&s->q_full, 9 * 16384);
-        tma_load_3d_pair(smem_u32(smem + kSmRopeQ), &qmap, in_cta(&s->q_full, rank), 0, row0, 8);
+        tma_load_3d_pair(smem_u32(smem + kSmRopeQ), &maps.q, in_cta(&s->q_full, rank), 0, row0, 8);
       }
       __syncwarp();
       for (int i = 0; i < 8 && claim(); ++i, ring.next()) {
         if (lane == 0)
-          tma_load_3d_pair(smem_u32(smem + ring.slot * kSlot), &qmap, in_cta(&s->q_full, rank), 0, row0, i);
+          tma_load_3d_pair(smem_u32(smem + ring.slot * kSlot), &maps.q, in_cta(&s->q_full, rank), 0, row0, i);
         __syncwarp();
       }
       Units u;
@@ -222,7 +205,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
         const Rows x = u.get(p, c, 2 * kt + a, lane, true);
         for (int k = 0; !F8 && k < 4 && claim(); ++k, ring.next()) {
           if (a == 0 && lane == 0) mbar_arrive_expect_tx(&s->full[ring.slot], 2 * kSlot);
-          load_keys(smem_u32(smem + ring.slot * kSlot), &kvmap, &rowmap, in_cta(&s->full[ring.slot], even), x,
+          load_keys(smem_u32(smem + ring.slot * kSlot), &maps.keys, &maps.row, in_cta(&s->full[ring.slot], even), x,
                     p.total_rows, 2 * k, 2, lane);
         }
         if (F8) ring.next(4);
@@ -230,7 +213,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
         ok = ok && (it < 2 || warp_wait(&s->s_full[buf], ((it >> 1) - 1) & 1));
         if (!ok) break;
         if (a == 0 && lane == 0) mbar_arrive_expect_tx(&s->rope_full[buf], 2 * 8192);
-        load_keys(smem_u32(smem + kSmRopeK + buf * 8192), &ropemap, &rowmap, in_cta(&s->rope_full[buf], even), x,
+        load_keys(smem_u32(smem + kSmRopeK + buf * 8192), &maps.rope, &maps.row, in_cta(&s->rope_full[buf], even), x,
                   p.total_rows, F8 ? 0 : 8, 1, lane);
       }
     }
@@ -248,7 +231,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
     const uint32_t full0 = in_cta(&s->full[0], even);
     Ring ring;
     Units u;
-    bool more = c.start(p, &s->run), ok = true;
+    bool more = c.start(p, run), ok = true;
     int kt = c.k0;
     CodePair code[2][2];  // [key][pair of slots]
     Rows x0{0, 0}, x1{0, 0};
@@ -308,7 +291,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
     // ---------------- all keys of each step, the own value dims
     Ring ring;
     bool ok = true;
-    for (bool more = !F8 && c.start(p, &s->run); more && ok; more = c.next(p)) {
+    for (bool more = !F8 && c.start(p, run); more && ok; more = c.next(p)) {
       Units u;
       u.start(p, c, lane, false);
       for (int kt = c.k0; kt < c.k1 && ok; ++kt) {
@@ -320,7 +303,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
             break;
           }
           if (a == 0 && lane == 0) mbar_arrive_expect_tx(&s->full[ring.slot], 2 * kSlot);
-          load_keys(smem_u32(smem + ring.slot * kSlot), &kvmap, &rowmap, in_cta(&s->full[ring.slot], even),
+          load_keys(smem_u32(smem + ring.slot * kSlot), &maps.keys, &maps.row, in_cta(&s->full[ring.slot], even),
                     k < 2 ? x0 : x1, p.total_rows, 2 * (2 * a + (k & 1)), 2, lane);
         }
       }
@@ -337,7 +320,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
       uint32_t phases = 0;  // of the slots' full barriers: q's uses of a slot do not count there
       bool ok = true;
       int it = 0, seg = 0;
-      for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
+      for (bool more = c.start(p, run); more && ok; more = c.next(p), ++seg) {
         ring.next(8);
         ok = warp_wait(&s->q_ready, seg & 1);
         for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
@@ -356,7 +339,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
               for (int st = 0; st < 8; ++st)
                 mma_bf16_ts_pair(d, q0 + st * 8, b0 + (((st >> 2) * 8192 + (st & 3) * 32) >> 4), k_hi, idesc,
                                  st > 0 ? 1u : acc0);
-              commit_to(&s->empty[ring.slot], 0x3);
+              mma_commit_to(&s->empty[ring.slot], 0x3);
             }
             __syncwarp();
           }
@@ -369,8 +352,8 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
 #pragma unroll
             for (int st = 0; st < 4; ++st)
               mma_bf16_ss_pair(d, k_lo + ((kSmRopeQ + st * 32) >> 4), k_hi, b0 + ((st * 32) >> 4), k_hi, idesc, 1u);
-            commit_to(&s->s_full[buf], 0x3);
-            if (last) commit_to(&s->q_rope_free, 0x3);
+            mma_commit_to(&s->s_full[buf], 0x3);
+            if (last) mma_commit_to(&s->q_rope_free, 0x3);
           }
           __syncwarp();
         }
@@ -390,7 +373,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
       Ring ring;
       bool ok = true;
       int it = 0;
-      for (bool more = c.start(p, &s->run); more && ok; more = c.next(p)) {
+      for (bool more = c.start(p, run); more && ok; more = c.next(p)) {
         for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
           const int buf = it & 1;
           ok = warp_wait(&s->p_ready[buf], (it >> 1) & 1);
@@ -414,9 +397,9 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
                 mma_bf16_ss_pair(tmem + 256, a0 + ((ks * 32) >> 4), p_hi, b1 + ((ks * 2048) >> 4), v_hi, idesc,
                                  ks > 0 ? 1u : acc0);
               }
-              commit_to(&s->empty[s0], 0xC);
-              commit_to(&s->empty[s1], 0xC);
-              if (kh == 1) commit_to(&s->pv_done[buf], 0xF);
+              mma_commit_to(&s->empty[s0], 0xC);
+              mma_commit_to(&s->empty[s1], 0xC);
+              if (kh == 1) mma_commit_to(&s->pv_done[buf], 0xF);
             }
             __syncwarp();
           }
@@ -432,7 +415,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
       const uint32_t alpha_dst = in_cta(smem + kSmAlpha, 2 + a);
       bool ok = true;
       int it = 0;
-      for (bool more = c.start(p, &s->run); more && ok; more = c.next(p)) {
+      for (bool more = c.start(p, run); more && ok; more = c.next(p)) {
         for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
           const int buf = it & 1;
           // P is staged, and its buffer there is free: PV of the step before the last is done
@@ -468,7 +451,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
       if (lane == 0) mbar_arrive(&s->maxima);
       return warp_wait(&s->maxima, meets++ & 1);
     };
-    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
+    for (bool more = c.start(p, run); more && ok; more = c.next(p), ++seg) {
       // q's latent dims -> tensor memory (the A operand); its slots are then free
       if (!warp_wait(&s->q_full, seg & 1)) {
         if (lane == 0) abort_now();
@@ -507,8 +490,8 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
       ring.slot = (ring.slot + 4 * ((c.k1 - c.k0) % kRing)) % kRing;  // the steps' slots
 
       const int in_tile = 128 * a + row;
-      const int tok = c.tile * p.tpt + in_tile / p.H;
-      const bool live = in_tile < p.tpt * p.H && tok < c.req.q_len;
+      const int tok = c.tile * p.tpt[1] + in_tile / p.H;
+      const bool live = in_tile < p.tpt[1] * p.H && tok < c.req.q_len;
       const int lim = live ? visible(c.req, tok) : 0;
       float m = kNegSentinel, l = 0.f;
       Units u;
@@ -617,7 +600,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
     const uint32_t p_ready = in_cta(&s->p_ready[0], 2), ml_free = in_cta(&s->ml_free, a);
     bool ok = true;
     int it = 0, seg = 0;
-    for (bool more = c.start(p, &s->run); more && ok; more = c.next(p), ++seg) {
+    for (bool more = c.start(p, run); more && ok; more = c.next(p), ++seg) {
       for (int kt = c.k0; kt < c.k1; ++kt, ++it) {
         const int buf = it & 1;
         if (tid == 0) mbar_arrive_expect_tx(&s->p_full[buf], 32768 + 512);
@@ -663,10 +646,10 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
       if (lane == 0) mbar_arrive_remote_relaxed(ml_free);
       tc_fence_after();
       const int in_tile = 128 * a + row;
-      const int tok = c.tile * p.tpt + in_tile / p.H;
-      const bool live = in_tile < p.tpt * p.H && tok < c.req.q_len;
+      const int tok = c.tile * p.tpt[1] + in_tile / p.H;
+      const bool live = in_tile < p.tpt[1] * p.H && tok < c.req.q_len;
       if (c.k0 == 0 && c.k1 == c.nk) {
-        const int64_t grow = static_cast<int64_t>(c.req.q0 + c.tile * p.tpt) * p.H + in_tile;
+        const int64_t grow = static_cast<int64_t>(c.req.q0 + c.tile * p.tpt[1]) * p.H + in_tile;
         const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
 #pragma unroll 1
         for (int q = 0; q < 256; q += 32) {  // columns 0-127 of a half: dims 128 half on; 128-255: 256 + 128 half on
@@ -704,18 +687,18 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
         if (half == 0) p.ml_part[slot * 256 + in_tile] = ml;
         if (c.k0 == 0 && rank == 2 && tid == 0) {
           // runs that hold the rest of this row tile
-          const int64_t at = s->run.end - c.left;
-          const int last = static_cast<int>((at + c.nk - 1) / s->run.per);
-          const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt) - c.tile * p.tpt) * p.H;
-          p.desc[quad] = make_int4((c.req.q0 + c.tile * p.tpt) * p.H, rows, last - quad, kQuadTile);
+          const int64_t at = run->end - c.left;
+          const int last = static_cast<int>((at + c.nk - 1) / run->per);
+          const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt[1]) - c.tile * p.tpt[1]) * p.H;
+          p.desc[quad] = make_int4((c.req.q0 + c.tile * p.tpt[1]) * p.H, rows, last - quad, 1);
         }
       }
       tc_fence_before();
     }
-    if (rank == 2 && tid == 0 && s->run.mine) {
+    if (rank == 2 && tid == 0) {
       // nothing to join: no row tile that starts in this run goes on behind it;
       // and the pair kernel's runs beyond leave nothing
-      if (!ok || s->run.pos >= s->run.end || c.k0 > 0 || c.k1 == c.nk) p.desc[quad] = make_int4(0, 0, 0, 0);
+      if (!ok || run->pos >= run->end || c.k0 > 0 || c.k1 == c.nk) p.desc[quad] = make_int4(0, 0, 0, 0);
       for (int i = quad + p.quads; i < p.pairs; i += p.quads) p.desc[i] = make_int4(0, 0, 0, 0);
     }
   }
@@ -730,6 +713,27 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
   cluster_sync_all();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// The lengths decide whether a cluster works as a quad or as two pairs.
+template <bool F8>
+__global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const __grid_constant__ DenseParams p,
+                                                                          const __grid_constant__ Maps quad_maps,
+                                                                          const __grid_constant__ Maps pair_maps) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // the tiles need it (without static arrays the dynamic part starts there)
+    if (threadIdx.x == 0) report(p.dev_status, DSA_DEVERR_TIMEOUT);
+    return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Run* run = reinterpret_cast<const Run*>(smem + kSmRun);
+  plan_run<kThreadsOf<F8>, true>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);
+  if (run->quad) {
+    run_quad<F8>(p, quad_maps, smem);
+  } else {
+    pairs::set_up<F8>(reinterpret_cast<pairs::Bars*>(smem + pairs::kSmBar), pair_maps);
+    pairs::run_pair<F8>(p, pair_maps, smem);
+  }
 }
 
 FuncAttrOnce g_smem[2];
@@ -768,29 +772,16 @@ int clusters_at_once() {
 }
 
 template <bool F8>
-dsa_status_t launch(const DenseParams& p, const void* q, const void* kv, int quads, cudaStream_t s) {
-  CUtensorMap qmap, kvmap, ropemap, rowmap;
-  const uint64_t rows = static_cast<uint64_t>(p.total_rows);
-  // rows of 9 blocks of 64 dims, block-major boxes; fp8: the rope dims only
-  // (128 bytes from byte 528 of a row)
-  const void* base = F8 ? static_cast<const uint8_t*>(kv) + kDv + 16 : kv;
-  const uint64_t blocks = F8 ? 1 : 9, row_bytes = F8 ? kF8Row : kDk * 2;
-  const uint64_t qstrides[2] = {kDk * 2, 128}, strides[2] = {row_bytes, 128};
-  const uint64_t qdims[3] = {64, static_cast<uint64_t>(p.T) * p.H, 9}, kvdims[3] = {64, rows, blocks};
-  const uint64_t rowdims[2] = {64 * blocks, rows};
-  const uint32_t qbox[3] = {64, 128, 1}, kvbox[3] = {64, 64, F8 ? 1u : 2u}, ropebox[3] = {64, 64, 1}, rowbox[2] = {64, 1};
-  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+dsa_status_t launch(const DenseParams& p, const void* q, const void* kv, cudaStream_t s) {
+  Maps quad_maps, pair_maps;
   dsa_status_t st;
-  if ((st = make_tmap(&qmap, bf16, 3, q, qdims, qstrides, qbox, sw)) != DSA_OK) return st;
-  if ((st = make_tmap(&kvmap, bf16, 3, base, kvdims, strides, kvbox, sw)) != DSA_OK) return st;
-  if ((st = make_tmap(&ropemap, bf16, 3, base, kvdims, strides, ropebox, sw)) != DSA_OK) return st;
-  if ((st = make_tmap(&rowmap, bf16, 2, base, rowdims, strides, rowbox, sw)) != DSA_OK) return st;
+  if ((st = make_maps(&quad_maps, p, F8, q, kv, 128, 1)) != DSA_OK) return st;
+  if ((st = make_maps(&pair_maps, p, F8, q, kv, 64, 9)) != DSA_OK) return st;
   if ((st = allow_smem(dense_mla_quad_kernel<F8>, kSmTotal, g_smem[F8])) != DSA_OK) return st;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  config<F8>(&cfg, attr, quads, s);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_quad_kernel<F8>, p, qmap, kvmap, ropemap, rowmap);
+  config<F8>(&cfg, attr, p.quads, s);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_quad_kernel<F8>, p, quad_maps, pair_maps);
   if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_quad_kernel launch failed: %s", cudaGetErrorString(e));
   return DSA_OK;
 }
@@ -809,8 +800,8 @@ int num_quads(bool f8) {
   return n - 1;
 }
 
-dsa_status_t launch_quads(const DenseParams& p, bool f8, const void* q, const void* kv, int quads, cudaStream_t s) {
-  return f8 ? launch<true>(p, q, kv, quads, s) : launch<false>(p, q, kv, quads, s);
+dsa_status_t launch_quads(const DenseParams& p, bool f8, const void* q, const void* kv, cudaStream_t s) {
+  return f8 ? launch<true>(p, q, kv, s) : launch<false>(p, q, kv, s);
 }
 
 }  // namespace dense

@@ -296,13 +296,13 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e != 0;
 }
-// The barrier at this offset of both CTAs receives an arrival when all prior
-// tcgen05 operations of this thread complete.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+// The barrier at this offset of every CTA in `ctas` (a mask of cluster ranks)
+// receives an arrival when all prior tcgen05 operations of this thread complete.
+__device__ __forceinline__ void mma_commit_to(uint64_t* bar, uint16_t ctas) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(ctas)
       : "memory");
 }
 // TMA loads into this CTA's shared memory that count their bytes on a barrier
