@@ -70,7 +70,7 @@ __device__ __forceinline__ void merge_tile(const DenseParams& p, const int4 d, i
       acc[i].w = fmaf(w, v.w, acc[i].w);
     }
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = den != 0.f ? 1.f / den : 0.f;
   const int64_t row = static_cast<int64_t>(d.x) + in_tile;
   uint4* dst = reinterpret_cast<uint4*>(p.out + row * kDv + dim);
 #pragma unroll
@@ -78,14 +78,41 @@ __device__ __forceinline__ void merge_tile(const DenseParams& p, const int4 d, i
     dst[e] = make_uint4(pack_bf16(acc[2 * e].x * inv, acc[2 * e].y * inv), pack_bf16(acc[2 * e].z * inv, acc[2 * e].w * inv),
                         pack_bf16(acc[2 * e + 1].x * inv, acc[2 * e + 1].y * inv),
                         pack_bf16(acc[2 * e + 1].z * inv, acc[2 * e + 1].w * inv));
-  if (dim == 0 && p.lse != nullptr) p.lse[row] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
+  if (dim == 0 && p.lse != nullptr) p.lse[row] = den != 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
+}
+
+// The kernel of few rows leaves them row by row: a block takes a row, a thread
+// four dims.
+__device__ __forceinline__ void merge_rows(const DenseParams& p, const int4 d, int run) {
+  const int row = blockIdx.x, parts = d.z + 1;
+  if (row >= d.y) return;
+  const auto slot = [&](int j) { return static_cast<int64_t>(j == 0 ? 2 * run + 1 : 2 * (run + j)) * p.single_rows + row; };
+  float M = kNegSentinel, den = 0.f;
+  for (int j = 0; j < parts; ++j) M = fmaxf(M, p.ml_part[slot(j)].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < parts; ++j) {
+    const float2 ml = p.ml_part[slot(j)];
+    const float4 v = p.o_part[slot(j) * (kDv / 4) + threadIdx.x];
+    const float w = exp2f(ml.x - M);
+    den = fmaf(w, ml.y, den);
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  const float inv = den != 0.f ? 1.f / den : 0.f;
+  const int64_t g = static_cast<int64_t>(d.x) + row;
+  reinterpret_cast<uint2*>(p.out + g * kDv)[threadIdx.x] =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (threadIdx.x == 0 && p.lse != nullptr) p.lse[g] = den != 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
 __global__ void __launch_bounds__(128) dense_mla_merge_kernel(const __grid_constant__ DenseParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 d = p.desc[blockIdx.y];
   if (d.z <= 0) return;
-  if (d.w) merge_tile<true>(p, d, blockIdx.y);
+  if (d.w == kSingle) merge_rows(p, d, blockIdx.y);
+  else if (d.w == kQuad) merge_tile<true>(p, d, blockIdx.y);
   else merge_tile<false>(p, d, blockIdx.y);
 }
 
@@ -99,7 +126,7 @@ __global__ void __launch_bounds__(pairs::threads(F8), 1) dense_mla_kernel(const 
   }
   pairs::set_up<F8>(reinterpret_cast<pairs::Bars*>(smem + pairs::kSmBar), maps);  // overlaps the kernel before
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_run<pairs::threads(F8), false>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);
+  plan_run<pairs::threads(F8), kPair>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);
   pairs::run_pair<F8>(p, maps, smem);
 }
 
@@ -107,10 +134,10 @@ FuncAttrOnce g_smem_dense[2], g_smem_merge;
 
 int num_pairs() { return std::max(1, num_sms() / 2); }
 // partials of 128 rows per pair; a quad's 256 rows take two pairs' worth, and
-// there are at most half as many
+// there are at most half as many; a single CTA's 32 rows take a quarter
 size_t o_part_bytes(int pairs) { return static_cast<size_t>(2 * pairs) * 128 * kDv * sizeof(float); }
 size_t ml_part_bytes(int pairs) { return static_cast<size_t>(2 * pairs) * 128 * sizeof(float2); }
-size_t workspace_bytes(int pairs) { return o_part_bytes(pairs) + ml_part_bytes(pairs) + pairs * sizeof(int4); }
+size_t workspace_bytes(int pairs) { return o_part_bytes(pairs) + ml_part_bytes(pairs) + num_sms() * sizeof(int4); }
 
 template <bool F8>
 dsa_status_t launch_pairs(const DenseParams& p, const void* q, const void* kv, cudaStream_t s) {
@@ -141,7 +168,7 @@ dsa_status_t launch_merge(const DenseParams& p, cudaStream_t s) {
   dsa_status_t st = allow_smem(dense_mla_merge_kernel, 0, g_smem_merge);
   if (st != DSA_OK) return st;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.quads > 0 ? 64 : 32, static_cast<unsigned>(p.pairs));
+  cfg.gridDim = p.singles > 0 ? dim3(p.single_rows, p.singles) : dim3(p.quads > 0 ? 64 : 32, p.pairs);
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -226,8 +253,16 @@ dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_st
   // not be cut: then a token's result must not depend on the other requests.
   d.quads = d.cut && static_cast<int64_t>(T) * H >= int64_t(256) * B ? num_quads(f8) : 0;
   d.pairs = d.quads > 0 ? 2 * d.quads : pairs;
-  if (d.quads > 0) st = launch_quads(d, f8, q, kv_cache, s);
-  else st = f8 ? launch_pairs<true>(d, q, kv_cache, s) : launch_pairs<false>(d, q, kv_cache, s);
+  d.single_rows = d.cut && !f8 ? single_rows(B, T, H) : 0;
+  if (d.single_rows > 0) {
+    d.singles = num_sms();
+    d.tpt[kSingle] = d.single_rows / H;
+    st = launch_singles(d, q, kv_cache, s);
+  } else if (d.quads > 0) {
+    st = launch_quads(d, f8, q, kv_cache, s);
+  } else {
+    st = f8 ? launch_pairs<true>(d, q, kv_cache, s) : launch_pairs<false>(d, q, kv_cache, s);
+  }
   if (st == DSA_OK && d.cut) st = launch_merge(d, s);
   return st == DSA_OK ? check_launch(name) : st;
 }

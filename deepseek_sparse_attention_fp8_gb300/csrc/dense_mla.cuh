@@ -28,15 +28,15 @@ constexpr int kSlot = 16384;  // 64 keys x 128 dims
 constexpr float kRescaleThreshold = 8.f;  // log2 units
 constexpr long long kWaitLimitCycles = 2000000000ll;
 constexpr int kAhead = 3;   // steps that the fp8 cache's rows are asked into L2 ahead
-constexpr int kMinRun = 4;  // steps a run has at least when row tiles may be cut
 
 struct DenseParams {
   int32_t num_blocks, rows_per_block, total_rows;
   const int32_t* block_table;
   int32_t bt_stride;
   const int32_t *seq_lens, *qsl;
-  int32_t B, T, H, tpt[2];   // tokens per row tile of a pair, of a quad
+  int32_t B, T, H, tpt[3];   // tokens per row tile of a pair, of a quad, of a single CTA
   int32_t pairs, quads;      // pairs and quads of CTAs launched; quads = 0: pairs only
+  int32_t singles, single_rows;  // single CTAs launched (the kernel of few rows), rows of their row tiles
   int32_t block_size, bs64;  // bs64 = block_size / 64
   float scale_log2;
   const uint8_t* kv;  // the fp8 cache
@@ -48,16 +48,17 @@ struct DenseParams {
   // from the run before, 2 n + 1 the one it leaves to the next
   float4* o_part;   // [slot][row halves][groups of 4 TMEM columns][128 lanes]
   float2* ml_part;  // [slot][rows of a row tile]: max (log2 units), sum
-  int4* desc;       // per run: the cut row tile that starts in it (first row, rows, further parts, quad)
+  int4* desc;       // per run: the cut row tile that starts in it (first row, rows, further parts, kind)
   int32_t* dev_status;
 };
 
 // The run of a group of CTAs: its first request, row tile and step, and its
 // steps [pos, end) of all; per: steps of every run. At the end of shared memory.
+enum Kind { kPair = 0, kQuad = 1, kSingle = 2 };
 struct Run {
   int32_t b, tile, k0, index;
   int64_t pos, end, per;
-  bool quad;  // the batch is worked on by quads
+  int32_t kind;  // what works on the batch
 };
 constexpr int kSmTotal = 232448, kSmRun = kSmTotal - 64;
 static_assert(sizeof(Run) <= 64, "run block too large");
@@ -126,13 +127,13 @@ __device__ __forceinline__ int64_t steps_before(const Request& r, int tpt, int n
 }
 
 // A run of steps, segment by segment (a segment: the steps of one row tile).
-template <bool QUAD>
+template <Kind KIND>
 struct Cursor {
   Request req;
   int32_t b, tile, nk, k0, k1;
   int32_t left;  // steps of the run from this segment on
   __device__ __forceinline__ void cut(const DenseParams& p) {
-    nk = steps_of(req, p.tpt[QUAD], tile);
+    nk = steps_of(req, p.tpt[KIND], tile);
     k1 = p.cut ? min(nk, k0 + left) : nk;
   }
   __device__ __forceinline__ bool start(const DenseParams& p, const Run* s) {
@@ -141,7 +142,7 @@ struct Cursor {
     k0 = k1 = nk = s->k0;
     left = static_cast<int32_t>(s->end - s->pos);
     if (left <= 0) return false;
-    req = load_request(p, p.tpt[QUAD], b);
+    req = load_request(p, p.tpt[KIND], b);
     cut(p);
     return true;
   }
@@ -153,7 +154,7 @@ struct Cursor {
       tile = 0;
       do {
         if (++b >= p.B) return false;
-        req = load_request(p, p.tpt[QUAD], b);
+        req = load_request(p, p.tpt[KIND], b);
       } while (req.n_tiles == 0);
     }
     cut(p);
@@ -289,13 +290,13 @@ __device__ __forceinline__ Decoded decode16(const CodePair& v, int g, bool swap)
 // The run of this pair or quad: every CTA sums the requests' steps itself.
 // `scratch` is shared memory that nothing else uses yet.
 //
-// QUADS: in clusters of four CTAs the lengths, which only the device knows,
+// kQuad: in clusters of four CTAs the lengths, which only the device knows,
 // decide here whether each cluster works as a quad or as two pairs. A row tile
 // costs a pair about 7100 + 4400 clocks a step (128 rows, 2 SMs), a quad 12300
 // + 2700 (256 rows, 4 SMs) and ~12000 more to begin with: fitted to 16 prompts
 // of 256 tokens (128 heads: 380 us on pairs, 477 on quads) and to 1024 tokens
 // over a context of 16384 (3580 and 2600 us).
-template <int kThreads, bool QUADS>
+template <int kThreads, Kind KIND>
 __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* scratch) {
   int64_t* sums = reinterpret_cast<int64_t*>(scratch);  // [4][warps]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -303,7 +304,7 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* 
   const bool once = p.B <= kThreads;
   int64_t total = 0;
   bool quad = false;
-  if constexpr (QUADS) {
+  if constexpr (KIND == kQuad) {
     int64_t tiles[2] = {0, 0}, steps[2] = {0, 0};
     for (int b = tid; b < p.B; b += kThreads) {
 #pragma unroll
@@ -329,8 +330,9 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* 
     quad = cost[1] * p.pairs + int64_t(120) * p.pairs * p.quads < cost[0] * p.quads;
     __syncthreads();
   }
-  const int tpt = p.tpt[quad];
-  const int index = quad ? blockIdx.x >> 2 : blockIdx.x >> 1, n_runs = quad ? p.quads : p.pairs;
+  const Kind kind = KIND == kSingle ? kSingle : quad ? kQuad : kPair;
+  const int tpt = p.tpt[kind], index = blockIdx.x >> (kind == kSingle ? 0 : kind == kQuad ? 2 : 1);
+  const int n_runs = kind == kSingle ? p.singles : kind == kQuad ? p.quads : p.pairs;
   int64_t w = 0, incl = 0;
   Request r = {};
   const auto scan = [&](int b, bool first) {  // steps of request b, and their inclusive sum over the block's requests
@@ -358,11 +360,15 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* 
   };
   for (int b0 = 0; b0 < p.B; b0 += kThreads) total += scan(b0 + tid, true);
   int64_t per = (total + n_runs - 1) / n_runs;
-  if (p.cut) per = max(per, int64_t(kMinRun));
+  // Runs of at least two steps (a request of 1000 keys, 128 heads: 27.8 us
+  // with the caches cold, 31.9 at four, 27.8 at one; 32 of 512 keys: 30.9
+  // at one, 29.9 at two), of one in the kernel of few rows (16 requests of 512
+  // keys: 20.6 us, 23.7 at two, 31 at four).
+  if (p.cut) per = max(per, int64_t(KIND == kSingle ? 1 : 2));
   const int64_t u0 = per * index, u1 = min(u0 + per, total);
   if (tid == 0) {
     s->index = index;
-    s->quad = quad;
+    s->kind = kind;
     s->per = per;
     s->pos = s->end = 0;
   }
@@ -435,6 +441,10 @@ int num_quads(bool f8);
 // Enqueues the kernel of clusters of four CTAs, p.quads of them, which work as
 // quads or as 2 p.quads = p.pairs pairs.
 dsa_status_t launch_quads(const DenseParams& p, bool f8, const void* q, const void* kv, cudaStream_t s);
+// Rows of a row tile in the kernel of few rows, 0 where that kernel does not
+// serve; enqueues it on p.singles CTAs.
+int single_rows(int32_t B, int32_t T, int32_t H);
+dsa_status_t launch_singles(const DenseParams& p, const void* q, const void* kv, cudaStream_t s);
 
 }  // namespace dense
 }  // namespace dsa

@@ -125,7 +125,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
       *reinterpret_cast<uint4*>(slot + (i ? (at0 + 512) ^ 64 : at0)) = v.first;
       *reinterpret_cast<uint4*>(slot + (i ? (at1 + 512) ^ 64 : at1)) = v.second;
     };
-    Cursor<false> c;
+    Cursor<kPair> c;
     bool more = c.start(p, run), ok = true;
     int kt = c.k0;
     CodePair own[2], oth[2];  // [key]
@@ -208,7 +208,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
     }
   } else if (!F8 && warp == kKeyWarp) {
     // ---------------- the own keys of each step, all 512 latent dims
-    Cursor<false> c;
+    Cursor<kPair> c;
     int it = 0;
     bool ok = true;
     for (bool more = c.start(p, run); more && ok; more = c.next(p)) {
@@ -242,7 +242,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
     // longer needs the dims they replace (CTA 1: after the first two slots,
     // CTA 0: after all), the rope dims of the next step's own keys, and q when
     // a row tile begins
-    Cursor<false> c;
+    Cursor<kPair> c;
     int it = 0;
     Rows other{0, 0};
     const auto load_other = [&](int i) {
@@ -275,7 +275,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
       __syncwarp();
     };
     for (bool more = c.start(p, run); more && ok; more = c.next(p)) {
-      const int row0 = (c.req.q0 + c.tile * p.tpt[0]) * p.H;
+      const int row0 = (c.req.q0 + c.tile * p.tpt[kPair]) * p.H;
       if (it == 0) load_q(row0);  // needs nothing else: ahead of the block table's entries
       Units u;
       u.start(p, c, lane, false);
@@ -316,7 +316,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
       const uint64_t dv = smem_desc(smem_u32(smem), 8192, 1024, kSwizzle128B);
       const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
       const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
-      Cursor<false> c;
+      Cursor<kPair> c;
       bool more = c.start(p, run);
       int iq = 0, ip = 0, sub = 0, half = 0, segs = 0;  // the next S and PV, and the parts of them
       int kt = c.k0;
@@ -404,7 +404,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
     // 1300-2000 clocks per step.)
     const uint32_t p_full = even(&s->p_full);
     uint8_t* p_dst = smem + kSmP + kh * 8192;
-    Cursor<false> c;
+    Cursor<kPair> c;
     int it = 0;
     uint32_t meets = 0;
     bool ok = true;
@@ -416,8 +416,8 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
     };
     for (bool more = c.start(p, run); more && ok; more = c.next(p)) {
       const int in_tile = 64 * r + row;  // row of the row tile
-      const int tok = c.tile * p.tpt[0] + in_tile / p.H;
-      const bool live = in_tile < p.tpt[0] * p.H && tok < c.req.q_len;
+      const int tok = c.tile * p.tpt[kPair] + in_tile / p.H;
+      const bool live = in_tile < p.tpt[kPair] * p.H && tok < c.req.q_len;
       const int lim = live ? visible(c.req, tok) : 0;
       float m = kNegSentinel, l = 0.f;
       Units u;
@@ -510,8 +510,8 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
       tc_fence_after();
       const uint32_t o_base = lane_base + kColO + 128 * half;
       if (c.k0 == 0 && c.k1 == c.nk) {
-        const int64_t grow = static_cast<int64_t>(c.req.q0 + c.tile * p.tpt[0]) * p.H + in_tile;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int64_t grow = static_cast<int64_t>(c.req.q0 + c.tile * p.tpt[kPair]) * p.H + in_tile;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
         uint16_t* dst = p.out + grow * kDv + 256 * kh + 128 * half;
 #pragma unroll 1
         for (int q = 0; q < 128; q += 32) {
@@ -534,7 +534,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
           __syncwarp();
         }
         if (live && kh == 0 && half == 0 && p.lse != nullptr)
-          p.lse[grow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          p.lse[grow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       } else {
         const int slot = 2 * pair + (c.k0 > 0 ? 0 : 1);
         float4* dst = p.o_part + (static_cast<int64_t>(2 * slot + r) * 64 + 32 * half) * 128 + l128;
@@ -552,8 +552,8 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
           // pairs whose runs hold the rest of this row tile
           const int64_t at = run->end - c.left;
           const int last = static_cast<int>((at + c.nk - 1) / run->per);
-          const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt[0]) - c.tile * p.tpt[0]) * p.H;
-          p.desc[pair] = make_int4((c.req.q0 + c.tile * p.tpt[0]) * p.H, rows, last - pair, 0);
+          const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt[kPair]) - c.tile * p.tpt[kPair]) * p.H;
+          p.desc[pair] = make_int4((c.req.q0 + c.tile * p.tpt[kPair]) * p.H, rows, last - pair, kPair);
         }
       }
       tc_fence_before();

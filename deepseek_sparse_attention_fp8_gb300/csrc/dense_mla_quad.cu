@@ -163,7 +163,7 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
   // a barrier's or buffer's address in another CTA
   const auto in_cta = [&](const void* x, int cta) { return mapa_shared(smem_u32(x), static_cast<uint32_t>(cta)); };
   const int even = rank & ~1;
-  Cursor<true> c;
+  Cursor<kQuad> c;
 
   if (warp == kLoadWarp && !values) {
     // ---------------- q of each row tile, then the own keys of its steps
@@ -176,7 +176,7 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
       return ok;
     };
     for (bool more = c.start(p, run); more && ok; more = c.next(p), ++seg) {
-      const int row0 = (c.req.q0 + c.tile * p.tpt[1]) * p.H + 128 * a;
+      const int row0 = (c.req.q0 + c.tile * p.tpt[kQuad]) * p.H + 128 * a;
       if (seg > 0 && !warp_wait(&s->q_rope_free, (seg - 1) & 1)) {
         ok = false;
         break;
@@ -490,8 +490,8 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
       ring.slot = (ring.slot + 4 * ((c.k1 - c.k0) % kRing)) % kRing;  // the steps' slots
 
       const int in_tile = 128 * a + row;
-      const int tok = c.tile * p.tpt[1] + in_tile / p.H;
-      const bool live = in_tile < p.tpt[1] * p.H && tok < c.req.q_len;
+      const int tok = c.tile * p.tpt[kQuad] + in_tile / p.H;
+      const bool live = in_tile < p.tpt[kQuad] * p.H && tok < c.req.q_len;
       const int lim = live ? visible(c.req, tok) : 0;
       float m = kNegSentinel, l = 0.f;
       Units u;
@@ -646,11 +646,11 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
       if (lane == 0) mbar_arrive_remote_relaxed(ml_free);
       tc_fence_after();
       const int in_tile = 128 * a + row;
-      const int tok = c.tile * p.tpt[1] + in_tile / p.H;
-      const bool live = in_tile < p.tpt[1] * p.H && tok < c.req.q_len;
+      const int tok = c.tile * p.tpt[kQuad] + in_tile / p.H;
+      const bool live = in_tile < p.tpt[kQuad] * p.H && tok < c.req.q_len;
       if (c.k0 == 0 && c.k1 == c.nk) {
-        const int64_t grow = static_cast<int64_t>(c.req.q0 + c.tile * p.tpt[1]) * p.H + in_tile;
-        const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+        const int64_t grow = static_cast<int64_t>(c.req.q0 + c.tile * p.tpt[kQuad]) * p.H + in_tile;
+        const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
 #pragma unroll 1
         for (int q = 0; q < 256; q += 32) {  // columns 0-127 of a half: dims 128 half on; 128-255: 256 + 128 half on
           uint32_t o[32];
@@ -671,7 +671,7 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
           }
           __syncwarp();
         }
-        if (live && half == 0 && p.lse != nullptr) p.lse[grow] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
+        if (live && half == 0 && p.lse != nullptr) p.lse[grow] = ml.y != 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
       } else {
         const int slot = 2 * quad + (c.k0 > 0 ? 0 : 1);
         float4* dst = p.o_part + (static_cast<int64_t>(2 * slot + a) * 128 + 64 * half) * 128 + row;
@@ -689,8 +689,8 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
           // runs that hold the rest of this row tile
           const int64_t at = run->end - c.left;
           const int last = static_cast<int>((at + c.nk - 1) / run->per);
-          const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt[1]) - c.tile * p.tpt[1]) * p.H;
-          p.desc[quad] = make_int4((c.req.q0 + c.tile * p.tpt[1]) * p.H, rows, last - quad, 1);
+          const int rows = (min(c.req.q_len, (c.tile + 1) * p.tpt[kQuad]) - c.tile * p.tpt[kQuad]) * p.H;
+          p.desc[quad] = make_int4((c.req.q0 + c.tile * p.tpt[kQuad]) * p.H, rows, last - quad, kQuad);
         }
       }
       tc_fence_before();
@@ -727,8 +727,8 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Run* run = reinterpret_cast<const Run*>(smem + kSmRun);
-  plan_run<kThreadsOf<F8>, true>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);
-  if (run->quad) {
+  plan_run<kThreadsOf<F8>, kQuad>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);
+  if (run->kind == kQuad) {
     run_quad<F8>(p, quad_maps, smem);
   } else {
     pairs::set_up<F8>(reinterpret_cast<pairs::Bars*>(smem + pairs::kSmBar), pair_maps);

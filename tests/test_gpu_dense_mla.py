@@ -122,6 +122,74 @@ def test_long_chunks_rising_scores():
     check(c)
 
 
+# few rows a request: one rank's share of the heads
+FEW_CASES = {
+    "h16": ([3000, 1, 64, 130, 8193, 127], [1] * 6, 16, 64),
+    "h32": ([5000, 129, 2, 128, 7777], [1] * 5, 32, 128),
+    "h17": ([999, 4000, 33], [1] * 3, 17, 64),
+    "h1": ([1, 700, 20000], [1] * 3, 1, 64),
+    "h5_three_tokens": ([2500, 3, 640], [3, 3, 3], 5, 64),
+    "h8_two_tokens": ([130, 2, 4500, 65], [2, 2, 2, 2], 8, 192),
+    "h16_two_tokens": ([4000, 70, 129], [2, 2, 2], 16, 64),
+    "a_prompt_among_tokens": ([1000, 30, 90, 2000, 5, 0, 300, 77], [1, 9, 1, 1, 1, 0, 1, 1], 16, 64),
+    "a_chunk_and_idle": ([6000] + [0] * 99, [90] + [0] * 99, 16, 64),
+    "one_cut_tile": ([60000], [1], 16, 256),
+    "many_short": ([(13 * i) % 500 + 1 for i in range(300)], [1] * 300, 32, 64),
+}
+
+
+@pytest.mark.parametrize("name", sorted(FEW_CASES))
+def test_few_rows(name):
+    lens, q_lens, H, block = FEW_CASES[name]
+    check(make_dense_case(lens, q_lens, H, block=block, seed=len(name)))
+
+
+@pytest.mark.parametrize("H", [16, 32])
+@pytest.mark.parametrize("q_std", [0.0, 300.0])
+def test_few_rows_score_ranges(H, q_std):
+    check(make_dense_case([7000, 5000, 90], [1, 1, 1], H, q_std=q_std, seed=41))
+
+
+@pytest.mark.parametrize("H", [16, 32])
+def test_few_rows_rising_scores(H):
+    c = make_dense_case([6000], [1], H, seed=42)
+    q = c["q"][0, 0].float()
+    n = (torch.arange(6000, device="cuda", dtype=torch.float32) / 50.0)[:, None]
+    rows = (q / q.pow(2).sum() / SCALE)[None, :] * n + 0.05 * torch.randn((6000, 576), device="cuda")
+    pages = torch.zeros((94, 64, 576), device="cuda")
+    pages.view(-1, 576)[:6000] = rows
+    c["cache"][c["table"][0].long()] = pages.to(torch.bfloat16)
+    c["q"][:, 1:] = c["q"][0, 0]
+    check(c)
+
+
+def test_few_rows_with_bad_blocks_and_lengths():
+    c = make_dense_case([6000, 1, 7000], [1, 2, 1], 16, seed=43, pad_tokens=3, extra_rows=8, extra_cols=2)
+    for b, j, v in ((0, 1, 10 ** 6), (0, 93, -5), (2, 40, int(c["cache"].shape[0])), (2, 109, -1)):
+        c["table"][b, j] = v
+    out, lse = check(c, status=api.DSA_DEVERR_BLOCK_OOB | api.DSA_DEVERR_SEQ_LEN,
+                     blocked={(0, 1), (0, 93), (2, 40), (2, 109)})
+    assert torch.isnan(out[4:]).all() and torch.isnan(lse[4:]).all()
+    assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,q_lens,H", [([500, 3000], [1, 1], 16), ([500, 3000], [1, 1], 128),
+                                           ([6000, 9000], [2, 4], 128)])
+def test_nan_stays_in_its_row(lens, q_lens, H, fp8):
+    """A head whose q is NaN, and one whose scores are infinite, leave the
+    other heads of the row tile as they are."""
+    c = make_dense_case(lens, q_lens, H, fp8=fp8, seed=44)
+    want, want_lse = check(c)
+    c["q"][0, 3] = float("nan")
+    c["q"][1, 7, 5] = float("inf")
+    out, lse, _ = call(c)
+    keep = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    keep[0, 3] = keep[1, 7] = False
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
+    assert torch.isnan(out[0, 3]).all() and torch.isnan(lse[0, 3])
+
+
 def test_captured_graph_follows_lengths_between_the_kernels():
     """Long and short contexts, chunks and none, in replays of one graph."""
     c = make_dense_case([9000, 7000], [8, 8], 128, seed=34)
