@@ -11,8 +11,8 @@
 // blocks alone. Latency bounds it: a launch, the lengths, the free ids, the
 // stores. When the queue's head is advanced in place the CTAs form one cluster,
 // whose barrier keeps the head until all have read it; else there are as many
-// as the tokens fill. (512 requests, 131000 tokens: one CTA 141 us, a cluster
-// of 8 18 us.)
+// as the tokens fill. From a graph, 512 requests with 131000 tokens: 7.0 us (a
+// cluster of 8: 18, one CTA: 141); 32 requests with a token each: 5.2 us.
 #include <algorithm>
 
 #include "common.cuh"

@@ -4,26 +4,18 @@
 //   s_i = scale * q[t,h,:] . kv[i,:]   for the keys i <= pos
 //   out = sum_i softmax(s)_i * kv[i, :512]     lse = log sum_i exp(s_i)
 //
-// Rows: the (token, head) rows of a request, 128 / H whole tokens at a time,
-// form row tiles of at most 128 rows; all of them see the same latent rows. A
-// row tile is worked on by a CTA pair, in steps of 128 keys:
-//   S = Q K^T   one cta_group::2 MMA, M = 128 (64 rows per CTA), N = 128:
-//               each CTA brings the 64 q rows it owns and 64 of the keys;
-//   softmax     thread = row and 32 keys; lazy rescaling of O (only when the
-//               row maximum grows by more than 2^8);
-//   O += P V    M = 128, N = 2 x 256: CTA r brings its rows of P and value
-//               dims [256 r, 256 r + 256) of all 128 keys.
-// CTA r needs all dims of its own 64 keys for S, and its own 256 dims of the
-// other 64 keys for O. The MMA takes the same offsets in both CTAs, so the
-// blocks of the other keys replace, after S, exactly those blocks of the own
-// keys that O does not need: a step holds 64 KB per CTA, and two steps are in
-// flight. A step moves 104 KB into each SM; at the ~32 bytes per clock that
-// an SM takes in (measured: 62 GB/s, whether from L2 or memory, multicast or
-// not) that is 3330 clocks, against 2180 of MMA: the copies bound it.
-//
-// Work: the steps of all row tiles form one sequence, cut into equal runs, one
-// per CTA pair (one persistent wave). A row tile cut by a run's end leaves
-// fp32 partials, at most two per pair, joined by dense_mla_merge_kernel.
+// Three kernels do it. All cut the batch's rows into row tiles (the rows of a
+// request see the same latent rows, whatever their head) and the row tiles'
+// steps of 128 keys into equal runs, one per group of CTAs, on the device:
+//   single CTAs    (dense_mla_rows.cu)  16 or 32 rows, keys along M: few rows a
+//                  request, memory bound;
+//   pairs          (here, dense_mla_pair.cuh)  128 rows: single tokens of many
+//                  heads, short prompts;
+//   clusters of 4  (dense_mla_quad.cu)  256 rows: chunks over long contexts;
+//                  they work as two pairs each where that is faster.
+// A row tile cut by a run's end leaves fp32 partials, at most two per run, which
+// dense_mla_merge_kernel joins. It reads 31 MB in ~5 us behind 32 requests of
+// 8192 keys and 128 heads, where every run of 27 steps is cut.
 #include <algorithm>
 
 #include "dense_mla_pair.cuh"
@@ -32,7 +24,6 @@ namespace dsa {
 namespace {
 
 using namespace dense;
-
 
 // Joins the partials of the row tile that starts in run blockIdx.y and goes on
 // behind it: out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j. A thread takes

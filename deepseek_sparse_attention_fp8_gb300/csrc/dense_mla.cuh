@@ -2,7 +2,7 @@
 // steps of 128 keys, cut into runs), its block table, and the loads of keys.
 //
 // Rows: the (token, head) rows of a request, whole tokens at a time, form row
-// tiles of at most 128 rows (256 in the four-CTA kernel); all rows of a request
+// tiles of at most 16, 32, 128 or 256 rows (by kernel); all rows of a request
 // see the same latent rows. The steps of all row tiles form one sequence, cut
 // into equal runs, one per group of CTAs (one persistent wave). A row tile cut
 // by a run's end leaves fp32 partials, at most two per run.

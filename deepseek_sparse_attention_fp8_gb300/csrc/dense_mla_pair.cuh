@@ -12,9 +12,20 @@
 // other 64 keys for O. The MMA takes the same offsets in both CTAs, so the
 // blocks of the other keys replace, after S, exactly those blocks of the own
 // keys that O does not need: a step holds 64 KB per CTA, and two steps are in
-// flight. A step moves 104 KB into each SM; at the ~32 bytes per clock that
-// an SM takes in (measured: 62 GB/s, whether from L2 or memory, multicast or
-// not) that is 3330 clocks, against 2180 of MMA: the copies bound it.
+// flight.
+//
+// What bounds it: an MMA of M = 128 on two CTAs runs at half the tensor rate
+// (measured: 131 clocks at N = 256, 82 at N = 128), 36 and 16 of them a step; a
+// step also moves 104 KB into each SM, 3330 clocks at the ~32 bytes a clock that
+// an SM takes in (measured: 62 GB/s, from L2 or memory, multicast or not). A
+// step takes 4400-4800 clocks. 32 requests of 8192 keys, 128 heads: 85 us; 8 of
+// 131072: 277 us (floors: 46 and 178 by bytes). Of the 85, about 10 pass until
+// the first S (the plan, the table, 208 KB from memory into every pair), 6 go
+// into partials and 5 into joining them.
+// With the fp8 cache the decoding warps bound it (42% of the issue slots of an
+// SM, chains of load, convert and store): 32 requests of 8192 keys 102 us;
+// without its loads 96 of then 113, without its stores 92, without asking rows
+// into L2 ahead 131.
 //
 // Work: the steps of all row tiles form one sequence, cut into equal runs, one
 // per CTA pair (one persistent wave). A row tile cut by a run's end leaves

@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kThreads) mla_kv_fp8_cache_kernel(const uint16
 
 // Producer side of the bf16 latent cache: token t's row goes to the slot the
 // caller gives. A copy of Dk bf16 per token, 16 bytes per thread; its floor is
-// the rows read and written once.
+// the rows read and written once: 16384 rows of 1152 bytes 5.6 us at the measured
+// copy rate, 6.0 us from a graph; 32 rows 1.6 us, a launch.
 __global__ void __launch_bounds__(kThreads) mla_kv_cache_kernel(const uint4* kv, int64_t kv_stride, int64_t n_chunks,
                                                                 int row_chunks, const int64_t* slot_map, uint4* cache,
                                                                 int64_t block_stride, int64_t n_slots, int block_size,
