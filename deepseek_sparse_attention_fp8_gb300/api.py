@@ -414,6 +414,16 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _empty(n, dtype, like, stream):
+    """Memory for a call on `stream`, which may be another than the current
+    one: taken from that stream's, so that no earlier use of it is unfinished
+    there and none begins before the call has ended."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=like.device)
+
+
 def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, free_blocks=None, free_head=None,
                     free_head_out=None, seq_lens=None, query_start_loc=None, token_req=None, positions=None,
                     slot_map=None, dev_status=None, stream=None):
@@ -438,15 +448,15 @@ def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, fre
         free_p = free_p or head_p  # an empty queue has no address of its own, and NULL would mean "take no blocks"
     n = max(max_tokens, 0)
     if seq_lens is None:
-        seq_lens = torch.empty(B, dtype=i32, device=ctx_lens.device)
+        seq_lens = _empty(B, i32, ctx_lens, stream)
     if query_start_loc is None:
-        query_start_loc = torch.empty(B + 1, dtype=i32, device=ctx_lens.device)
+        query_start_loc = _empty(B + 1, i32, ctx_lens, stream)
     if token_req is None:
-        token_req = torch.empty(n, dtype=i32, device=ctx_lens.device)
+        token_req = _empty(n, i32, ctx_lens, stream)
     if positions is None:
-        positions = torch.empty(n, dtype=i32, device=ctx_lens.device)
+        positions = _empty(n, i32, ctx_lens, stream)
     if slot_map is None:
-        slot_map = torch.empty(n, dtype=torch.int64, device=ctx_lens.device)
+        slot_map = _empty(n, torch.int64, ctx_lens, stream)
     outs = (seq_lens, query_start_loc, token_req, positions, slot_map)
     seq_p, qsl_p = _arg(seq_lens, i32, 1, "seq_lens", dev), _arg(query_start_loc, i32, 1, "query_start_loc", dev)
     req_p, pos_p = _arg(token_req, i32, 1, "token_req", dev), _arg(positions, i32, 1, "positions", dev)
@@ -515,7 +525,7 @@ def _dense_mla(name, call, q, kv_cache, cache_dtype, block_table, seq_lens, quer
         if workspace is not None:
             ws_bytes = workspace.numel() * workspace.element_size()
         if ws_bytes < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _empty(need, torch.uint8, q, stream)
             ws_bytes = need
         if workspace is not None:
             ws_p = _arg(workspace, workspace.dtype, workspace.dim(), "workspace", dev)

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const __grid_cons
     __syncthreads();
     const int first = s_start[0], end = s_start[n];
     // four tokens from a multiple of 4 on; the chunk may begin and end inside
-    for (int64_t t0 = (first & ~3) + 4 * (rank * kThreads + tid); t0 < end; t0 += 4 * step) {
+    for (int64_t t0 = (first & ~3) + int64_t(4) * (rank * kThreads + tid); t0 < end; t0 += 4 * step) {
       const int ta = max(static_cast<int>(t0), first);
       int lo = 0, hi = n - 1;  // the last request that starts at or before the first token
       while (lo < hi) {
@@ -243,9 +243,10 @@ extern "C" dsa_status_t dsa_build_batch(const int32_t* ctx_lens, const int32_t* 
   p.dev_status = dev_status;
   p.vec = aligned16(token_req) && aligned16(positions) && aligned16(slot_map);
   const bool in_place = free_blocks && free_head == free_head_out;
-  const int ctas = std::min((max_tokens + kThreads * 4 - 1) / (kThreads * 4), in_place ? kCluster : num_sms());
+  const int64_t fill = (int64_t(max_tokens) + kThreads * 4 - 1) / (kThreads * 4);
+  const int64_t ctas = std::min<int64_t>(fill, in_place ? kCluster : num_sms());
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max(ctas, 1)));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(ctas, 1)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];

@@ -111,10 +111,7 @@ template <bool F8>
 __global__ void __launch_bounds__(pairs::threads(F8), 1) dense_mla_kernel(const __grid_constant__ DenseParams p,
                                                                           const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  if (smem_u32(smem) & 1023u) {  // the tiles need it (without static arrays the dynamic part starts there)
-    if (threadIdx.x == 0) report(p.dev_status, DSA_DEVERR_TIMEOUT);
-    return;
-  }
+  if (misaligned(p, smem)) return;
   pairs::set_up<F8>(reinterpret_cast<pairs::Bars*>(smem + pairs::kSmBar), maps);  // overlaps the kernel before
   asm volatile("griddepcontrol.wait;" ::: "memory");
   plan_run<pairs::threads(F8), kPair>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);
@@ -203,7 +200,7 @@ dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_st
   if (kv_block_stride % row)
     return fail(DSA_ERR_UNSUPPORTED, "%s: kv_block_stride %lld is not a whole number of %lld-unit rows", name,
                 static_cast<long long>(kv_block_stride), static_cast<long long>(row));
-  if (num_blocks * (kv_block_stride / row) >= (int64_t(1) << 31))
+  if (kv_block_stride / row >= (int64_t(1) << 31) || num_blocks * (kv_block_stride / row) >= (int64_t(1) << 31))
     return fail(DSA_ERR_UNSUPPORTED, "%s: the cache holds 2^31 rows or more", name);
   dsa_status_t st = check_device();
   if (st != DSA_OK) return st;

@@ -63,6 +63,18 @@ struct Run {
 constexpr int kSmTotal = 232448, kSmRun = kSmTotal - 64;
 static_assert(sizeof(Run) <= 64, "run block too large");
 
+// The tiles need 1024-byte alignment (without static arrays the dynamic part of
+// shared memory starts there). Without it the call does nothing, and there is
+// nothing to join.
+__device__ __forceinline__ bool misaligned(const DenseParams& p, const uint8_t* smem) {
+  if ((smem_u32(smem) & 1023u) == 0) return false;
+  if (threadIdx.x == 0) {
+    report(p.dev_status, DSA_DEVERR_TIMEOUT);
+    if (p.cut && blockIdx.x < max(p.pairs, p.singles)) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  return true;
+}
+
 // A request's rows as work: row tile i has steps(i) = max(1, ceil(keys its
 // last token sees / 128)).
 struct Request {

@@ -728,10 +728,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
                                                                           const __grid_constant__ Maps quad_maps,
                                                                           const __grid_constant__ Maps pair_maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  if (smem_u32(smem) & 1023u) {  // the tiles need it (without static arrays the dynamic part starts there)
-    if (threadIdx.x == 0) report(p.dev_status, DSA_DEVERR_TIMEOUT);
-    return;
-  }
+  if (misaligned(p, smem)) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Run* run = reinterpret_cast<const Run*>(smem + kSmRun);
   plan_run<kThreadsOf<F8>, kQuad>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);

@@ -84,10 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_rows_kernel(const __gri
                                                                      const __grid_constant__ Maps maps) {
   using L = Layout<N>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  if (smem_u32(smem) & 1023u) {  // the tiles need it (without static arrays the dynamic part starts there)
-    if (threadIdx.x == 0) report(p.dev_status, DSA_DEVERR_TIMEOUT);
-    return;
-  }
+  if (misaligned(p, smem)) return;
   Bars* s = reinterpret_cast<Bars*>(smem + L::kBar);
   const Run* run = reinterpret_cast<const Run*>(smem + kSmRun);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -349,6 +349,27 @@ def test_captured_graph_follows_new_lengths():
         check_dense(out[:sum(q_lens)], lse[:sum(q_lens)], dense_reference(now))
 
 
+def test_own_workspace_on_another_stream():
+    """The workspace a call takes itself is not given to the current stream
+    while the call still waits on its own."""
+    c = make_dense_case([9000, 3000], [1, 1], 128, seed=51)
+    n = api.dense_mla_workspace_size(2, 128, DV, 0)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    out = torch.full((2, 128, DV), float("nan"), dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lse = torch.empty((2, 128), device="cuda")
+    torch.cuda.current_stream().synchronize()
+    api.dense_mla_attention(c["q"], c["cache"], c["table"], c["seq"], c["qsl"], SCALE, DV, out, lse=lse,
+                            dev_status=st, stream=s)
+    other = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and all(int(o.max().item()) == 0 for o in other)
+    check_dense(out, lse, dense_reference(c))
+
+
 def test_two_calls_at_once_with_a_workspace_each():
     cs = [make_dense_case([4000 + 100 * i, 700], [1, 3], 128, seed=20 + i, fp8=bool(i)) for i in range(2)]
     ws = [torch.empty(max(16, api.dense_mla_workspace_size(4, 128, DV, 0)), dtype=torch.uint8, device="cuda")
