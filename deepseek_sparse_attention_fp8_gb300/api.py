@@ -405,6 +405,17 @@ def _arg(t, dtype, dims, name, dev):
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
+def _vec(t, dtype, n, name, dev):
+    """_arg of a vector of at least n elements."""
+    try:
+        if (t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.dim() == 1 and t.numel() >= n):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _arg(t, dtype, 1, name, dev)
+    raise ValueError(f"{name} needs {n} elements, has {t.shape[0]}")
+
+
 def _status_arg(dev_status, dev):
     return None if dev_status is None else _arg(dev_status, torch.int32, dev_status.dim(), "dev_status", dev)
 
@@ -433,18 +444,17 @@ def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, fre
     the queue free_blocks, from *free_head on; free_head_out (default: in
     place) receives the advanced head."""
     i32, dev = torch.int32, torch.cuda.current_device()
-    ctx_p, new_p = _arg(ctx_lens, i32, 1, "ctx_lens", dev), _arg(new_lens, i32, 1, "new_lens", dev)
+    ctx_p, new_p = _vec(ctx_lens, i32, 0, "ctx_lens", dev), _vec(new_lens, i32, 0, "new_lens", dev)
     table_p = _arg(block_table, i32, 2, "block_table", dev)
-    B = ctx_lens.shape[0]
-    if new_lens.shape[0] != B or block_table.shape[0] < B:
+    B = ctx_lens.numel()
+    table_rows, table_cols = block_table.shape
+    if new_lens.numel() != B or table_rows < B:
         raise ValueError("new_lens and block_table must have a row per request of ctx_lens")
     free_p = head_p = head_out_p = None
     if free_blocks is not None:
         free_head_out = free_head if free_head_out is None else free_head_out
-        free_p = _arg(free_blocks, i32, 1, "free_blocks", dev)
-        head_p, head_out_p = _arg(free_head, i32, 1, "free_head", dev), _arg(free_head_out, i32, 1, "free_head_out", dev)
-        if not head_p or not head_out_p:
-            raise ValueError("free_head and free_head_out must have an element")
+        free_p = _vec(free_blocks, i32, 0, "free_blocks", dev)
+        head_p, head_out_p = _vec(free_head, i32, 1, "free_head", dev), _vec(free_head_out, i32, 1, "free_head_out", dev)
         free_p = free_p or head_p  # an empty queue has no address of its own, and NULL would mean "take no blocks"
     n = max(max_tokens, 0)
     if seq_lens is None:
@@ -457,19 +467,14 @@ def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, fre
         positions = _empty(n, i32, ctx_lens, stream)
     if slot_map is None:
         slot_map = _empty(n, torch.int64, ctx_lens, stream)
-    outs = (seq_lens, query_start_loc, token_req, positions, slot_map)
-    seq_p, qsl_p = _arg(seq_lens, i32, 1, "seq_lens", dev), _arg(query_start_loc, i32, 1, "query_start_loc", dev)
-    req_p, pos_p = _arg(token_req, i32, 1, "token_req", dev), _arg(positions, i32, 1, "positions", dev)
-    slot_p = _arg(slot_map, torch.int64, 1, "slot_map", dev)
-    for t, need, name in zip(outs, (B, B + 1, n, n, n), ("seq_lens", "query_start_loc", "token_req", "positions",
-                                                         "slot_map")):
-        if t.shape[0] < need:
-            raise ValueError(f"{name} needs {need} elements, has {t.shape[0]}")
-    st = lib.dsa_build_batch(ctx_p, new_p, B, block_size, free_p, 0 if free_blocks is None else free_blocks.shape[0],
-                             head_p, head_out_p, table_p, block_table.shape[1], max_tokens, seq_p, qsl_p, req_p, pos_p,
+    seq_p, qsl_p = _vec(seq_lens, i32, B, "seq_lens", dev), _vec(query_start_loc, i32, B + 1, "query_start_loc", dev)
+    req_p, pos_p = _vec(token_req, i32, n, "token_req", dev), _vec(positions, i32, n, "positions", dev)
+    slot_p = _vec(slot_map, torch.int64, n, "slot_map", dev)
+    st = lib.dsa_build_batch(ctx_p, new_p, B, block_size, free_p, 0 if free_blocks is None else free_blocks.numel(),
+                             head_p, head_out_p, table_p, table_cols, max_tokens, seq_p, qsl_p, req_p, pos_p,
                              slot_p, _status_arg(dev_status, dev), _raw_stream(stream, dev))
     _check(st, "dsa_build_batch")
-    return outs
+    return seq_lens, query_start_loc, token_req, positions, slot_map
 
 
 def dsa_mla_kv_cache(kv, slot_map, kv_cache, dev_status=None, stream=None):
