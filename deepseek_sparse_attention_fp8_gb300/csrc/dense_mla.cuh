@@ -217,6 +217,22 @@ struct Units {
     if (left <= 0 || first < 0) return {p.total_rows, 0};
     return {first, min(left, 64)};
   }
+  // one of a step's two units
+  template <class C>
+  __device__ __forceinline__ Rows of(const DenseParams& p, const C& c, int kt, int which) const {
+    const int left = c.req.kv_len - kt * kTile - 64 * which;
+    const int32_t first = __shfl_sync(0xFFFFFFFFu, row, (2 * kt - base + which) & 31);
+    return {first < 0 ? p.total_rows : first, first < 0 ? 0 : min(left, 64)};  // (no rows with n < 0 either)
+  }
+  // makes the units of step kt those that `of` finds; steps in ascending order
+  template <class C>
+  __device__ __forceinline__ void advance(const DenseParams& p, const C& c, int kt, int lane, bool rep) {
+    if (2 * kt >= base + 32) {
+      base += 32;
+      row = first_row(p, c, ahead, base + lane, rep);
+      ahead = entry(p, c, base + 32 + lane);
+    }
+  }
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -277,7 +293,7 @@ struct CodePair {
   uint4 c[2];
   float2 sc;
 };
-__device__ __forceinline__ CodePair fetch_pair(const uint8_t* row, int group, int lane8, bool exists) {
+__device__ __forceinline__ CodePair fetch_pair(const uint8_t* codes, const uint8_t* scales, bool exists) {
   CodePair v{{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, make_float2(0.f, 0.f)};
   if (exists) {
     // volatile: issued here, ahead of the waits, not where the values are used
@@ -285,8 +301,8 @@ __device__ __forceinline__ CodePair fetch_pair(const uint8_t* row, int group, in
     for (int g = 0; g < 2; ++g)
       asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(v.c[g].x), "=r"(v.c[g].y), "=r"(v.c[g].z), "=r"(v.c[g].w)
-                   : "l"(row + 128 * (group + g) + 16 * lane8));
-    asm volatile("ld.global.nc.v2.f32 {%0, %1}, [%2];" : "=f"(v.sc.x), "=f"(v.sc.y) : "l"(row + kDv + 4 * group));
+                   : "l"(codes + 128 * g));
+    asm volatile("ld.global.nc.v2.f32 {%0, %1}, [%2];" : "=f"(v.sc.x), "=f"(v.sc.y) : "l"(scales));
   }
   return v;
 }

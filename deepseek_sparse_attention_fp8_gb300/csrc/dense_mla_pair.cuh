@@ -153,14 +153,14 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint8_t* row = p.kv + static_cast<int64_t>(x.row + key + 4 * i) * kF8Row;
-        own[i] = fetch_pair(row, 2 * h, lane8, key + 4 * i < x.n);
+        own[i] = fetch_pair(row + 256 * h + 16 * lane8, row + kDv + 8 * h, key + 4 * i < x.n);
       }
     };
     const auto fetch_other = [&](const Rows& xo) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint8_t* row = p.kv + static_cast<int64_t>(xo.row + key + 4 * i) * kF8Row;
-        oth[i] = fetch_pair(row, 2 * r, lane8, key + 4 * i < xo.n);
+        oth[i] = fetch_pair(row + 256 * r + 16 * lane8, row + kDv + 8 * r, key + 4 * i < xo.n);
       }
     };
     if (more) {

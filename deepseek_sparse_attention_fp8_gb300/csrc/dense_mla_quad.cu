@@ -244,16 +244,24 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
     Rows x0{0, 0}, x1{0, 0};
     const auto locate = [&] {
       if (kt == c.k0) u.start(p, c, lane, false);
-      x0 = u.get(p, c, 2 * kt, lane, false);
-      x1 = u.get(p, c, 2 * kt + 1, lane, false);
-      if (!values && a) x0 = x1;
+      else u.advance(p, c, kt, lane, false);
+      x0 = u.of(p, c, kt, values ? 0 : a);
+      if (values) x1 = u.of(p, c, kt, 1);
     };
+    // this lane's codes in a row `key`, and from there to the scales
+    const uint8_t* const lane_codes = p.kv + key * kF8Row + 16 * lane8 + (values ? 256 * a : 0);
+    const int to_scales = kDv - 16 * lane8 - (values ? 248 * a : 0);
     const auto fetch = [&](int h) {
       const Rows& x = values && h ? x1 : x0;
+      const uint8_t* row = lane_codes + static_cast<int64_t>(x.row) * kF8Row;
+      const uint8_t* scales = row + to_scales;
+      if (!values) {
+        row += 256 * h;
+        scales += 8 * h;
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        code[i][h] = fetch_pair(p.kv + static_cast<int64_t>(x.row + key + 4 * i) * kF8Row, values ? 2 * a : 2 * h, lane8,
-                                key + 4 * i < x.n);
+        code[i][h] = fetch_pair(row + 4 * i * kF8Row, scales + 4 * i * kF8Row, key + 4 * i < x.n);
     };
     if (more) {
       locate();
