@@ -19,9 +19,11 @@
 // heads) 2.67 ms, 1.69 PFLOP/s or 0.91 of the measured tensor rate, with 9.0
 // TB/s taken in by the 144 SMs in use: both are nearly full (pairs: 3.58 ms).
 // With the fp8 cache CTAs 0, 1 decode their 64 keys, CTAs 2, 3 their dims of
-// all keys: ~3400 clocks a step, bound by the decoding warps' chains of load,
-// convert and store (47% of the issue slots; tensor cores at 44%). Five chunks
-// of up to 700 tokens over up to 9000 keys: 1.8 ms.
+// all keys: ~3500 clocks a step. Five chunks of up to 700 tokens over up to
+// 9000 keys: 1.80 ms. The MMAs of S then take 96 clocks instead of 64 each:
+// codes, decoded tiles, P and the MMAs' operands all pass through an SM's
+// shared memory. Without the loads of codes (and with the same decoding) it is
+// 1.43 ms; codes brought by TMA and read from shared memory 1.92.
 #include <algorithm>
 
 #include "dense_mla_pair.cuh"
