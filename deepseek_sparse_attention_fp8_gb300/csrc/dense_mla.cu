@@ -241,11 +241,11 @@ dsa_status_t dense_impl(const void* q, const void* kv_cache, int64_t kv_block_st
   // not be cut: then a token's result must not depend on the other requests.
   d.quads = d.cut && static_cast<int64_t>(T) * H >= int64_t(256) * B ? num_quads(f8) : 0;
   d.pairs = d.quads > 0 ? 2 * d.quads : pairs;
-  d.single_rows = d.cut && !f8 ? single_rows(B, T, H) : 0;
+  d.single_rows = d.cut ? single_rows(B, T, H, f8) : 0;
   if (d.single_rows > 0) {
     d.singles = num_sms();
     d.tpt[kSingle] = d.single_rows / H;
-    st = launch_singles(d, q, kv_cache, s);
+    st = launch_singles(d, f8, q, kv_cache, s);
   } else if (d.quads > 0) {
     st = launch_quads(d, f8, q, kv_cache, s);
   } else {

@@ -289,6 +289,7 @@ __device__ __forceinline__ uint4 decode8(uint32_t a, uint32_t b, float sc) {
 // where the key does not exist. The upper four lanes of a key write another
 // 64-dim block than the lower four, in the same banks: they store their two
 // 16-byte chunks in the other order.
+__device__ __forceinline__ uint4 decode8(uint2 c, float sc) { return decode8(c.x, c.y, sc); }
 struct CodePair {
   uint4 c[2];
   float2 sc;
@@ -309,9 +310,7 @@ __device__ __forceinline__ CodePair fetch_pair(const uint8_t* codes, const uint8
 struct Decoded {
   uint4 first, second;
 };
-__device__ __forceinline__ Decoded decode16(const CodePair& v, int g, bool swap) {
-  const uint4& c = v.c[g];
-  const float sc = g ? v.sc.y : v.sc.x;
+__device__ __forceinline__ Decoded decode16(const uint4& c, float sc, bool swap) {
   return {decode8(swap ? c.z : c.x, swap ? c.w : c.y, sc), decode8(swap ? c.x : c.z, swap ? c.y : c.w, sc)};
 }
 
@@ -446,6 +445,10 @@ __device__ __forceinline__ void plan_run(const DenseParams& p, Run* s, uint8_t* 
 struct Maps {
   CUtensorMap q, keys, rope, row;
 };
+// fp8: 64 rows' codes of a group, and their 16 bytes of scales.
+struct CodeMaps {
+  CUtensorMap codes, scales;
+};
 inline dsa_status_t make_maps(Maps* m, const DenseParams& p, bool f8, const void* q, const void* kv, uint32_t q_rows,
                               uint32_t q_blocks) {
   const void* base = f8 ? static_cast<const uint8_t*>(kv) + kDv + 16 : kv;
@@ -464,6 +467,14 @@ inline dsa_status_t make_maps(Maps* m, const DenseParams& p, bool f8, const void
   return make_tmap(&m->row, bf16, 2, base, row_dims, strides, row_box, sw);
 }
 
+inline dsa_status_t make_code_maps(CodeMaps* m, const DenseParams& p, const void* kv) {
+  const uint64_t dims[2] = {kF8Row, static_cast<uint64_t>(p.total_rows)}, strides[1] = {kF8Row};
+  const uint32_t codes[2] = {128, 64}, scales[2] = {16, 64};
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const dsa_status_t st = make_tmap(&m->codes, u8, 2, kv, dims, strides, codes, CU_TENSOR_MAP_SWIZZLE_NONE);
+  return st != DSA_OK ? st : make_tmap(&m->scales, u8, 2, kv, dims, strides, scales, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 // Number of 4-CTA clusters the current device runs at once, 0 when it cannot.
 int num_quads(bool f8);
 // Enqueues the kernel of clusters of four CTAs, p.quads of them, which work as
@@ -471,8 +482,8 @@ int num_quads(bool f8);
 dsa_status_t launch_quads(const DenseParams& p, bool f8, const void* q, const void* kv, cudaStream_t s);
 // Rows of a row tile in the kernel of few rows, 0 where that kernel does not
 // serve; enqueues it on p.singles CTAs.
-int single_rows(int32_t B, int32_t T, int32_t H);
-dsa_status_t launch_singles(const DenseParams& p, const void* q, const void* kv, cudaStream_t s);
+int single_rows(int32_t B, int32_t T, int32_t H, bool f8);
+dsa_status_t launch_singles(const DenseParams& p, bool f8, const void* q, const void* kv, cudaStream_t s);
 
 }  // namespace dense
 }  // namespace dsa

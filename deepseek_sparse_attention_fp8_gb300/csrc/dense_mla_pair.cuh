@@ -182,7 +182,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(oth[i], g, swap));
+            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(oth[i].c[g], g ? oth[i].sc.y : oth[i].sc.x, swap));
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -194,7 +194,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(own[i], g, swap));
+            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(own[i].c[g], g ? own[i].sc.y : own[i].sc.x, swap));
           }
           fence_proxy_async_smem();
           __syncwarp();

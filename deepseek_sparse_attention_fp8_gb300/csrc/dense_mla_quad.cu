@@ -54,6 +54,7 @@ static_assert(kSmBar + 448 <= kSmRun && kSmMl + 1024 <= kSmBar, "shared memory")
 
 struct Bars {  // at the same offset in every CTA
   uint64_t full[kRing], empty[kRing];  // ring slots; full: of both CTAs of a pair, the even one's barrier
+  uint64_t codes[kRing];               // fp8: a slot's codes landed
   // CTAs 0, 1
   uint64_t q_full, q_copied;  // q landed in the ring; copied to tensor memory by this CTA's warps
   uint64_t q_ready;           // ... by both CTAs' (CTA 0's barrier)
@@ -116,7 +117,8 @@ struct Ring {
 
 // Works on this quad's run, and ends with a cluster barrier.
 template <bool F8>
-__device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps, uint8_t* smem) {
+__device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps, const CodeMaps& code_maps,
+                                         uint8_t* smem) {
   Bars* s = reinterpret_cast<Bars*>(smem + kSmBar);
   const Run* run = reinterpret_cast<const Run*>(smem + kSmRun);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -128,6 +130,7 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&s->full[i], F8 ? 2 * kDecodeWarps : 1);
       mbar_init(&s->empty[i], 1);
+      mbar_init(&s->codes[i], 1);
     }
     mbar_init(&s->q_full, 1);
     mbar_init(&s->q_copied, kWorkers);
@@ -172,11 +175,19 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
   // a barrier's or buffer's address in another CTA
   const auto in_cta = [&](const void* x, int cta) { return mapa_shared(smem_u32(x), static_cast<uint32_t>(cta)); };
   const int even = rank & ~1;
+  // fp8: 64 keys' codes of a group, to where their dims 64-127 will be
+  const auto load_codes = [&](int slot, int group, int row) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&s->codes[slot], 8192);
+      tma_load_2d(smem_u32(smem + slot * kSlot + 8192), &code_maps.codes, &s->codes[slot], 128 * group, row);
+    }
+    __syncwarp();
+  };
   Cursor<kQuad> c;
 
   if (warp == kLoadWarp && !values) {
-    // ---------------- q of each row tile, then the own keys of its steps
-    // (fp8: their rope dims; the rest is decoded)
+    // ---------------- q of each row tile, then the own keys of its steps (fp8:
+    // the codes of the latent dims)
     Ring ring;
     bool ok = true;
     int it = 0, seg = 0;
@@ -202,22 +213,18 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
       }
       Units u;
       u.start(p, c, lane, true);
-      Units far = u;
-      const auto ask = [&](int kt) {  // fp8: the decoding warps' loads find the rows in L2
-        const Rows x = far.get(p, c, 2 * kt + a, lane, false);
-        if (x.n > 0 && lane == 0) prefetch_l2(p.kv + static_cast<int64_t>(x.row) * kF8Row, x.n * kF8Row);
-      };
-      for (int kt = c.k0; F8 && kt < min(c.k0 + kAhead, c.k1); ++kt) ask(kt);
       for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
         const int buf = it & 1;
-        if (F8 && kt + kAhead < c.k1) ask(kt + kAhead);
         const Rows x = u.get(p, c, 2 * kt + a, lane, true);
-        for (int k = 0; !F8 && k < 4 && claim(); ++k, ring.next()) {
+        for (int k = 0; k < 4 && claim(); ++k, ring.next()) {
+          if constexpr (F8) {
+            load_codes(ring.slot, k, x.row);
+            continue;
+          }
           if (a == 0 && lane == 0) mbar_arrive_expect_tx(&s->full[ring.slot], 2 * kSlot);
           load_keys(smem_u32(smem + ring.slot * kSlot), &maps.keys, &maps.row, in_cta(&s->full[ring.slot], even), x,
                     p.total_rows, 2 * k, 2, lane);
         }
-        if (F8) ring.next(4);
         // the rope dims: their buffer is free with S of the step before the last
         ok = ok && (it < 2 || warp_wait(&s->s_full[buf], ((it >> 1) - 1) & 1));
         if (!ok) break;
@@ -231,76 +238,90 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
   } else if (F8 && warp >= kDecodeWarp) {
     // ---------------- fp8: a step's 4 slots of 64 keys x 128 dims (CTAs 0, 1:
     // the 4 groups of the own keys; CTAs 2, 3: the 2 own groups of both units
-    // of keys), 8 keys per warp. The registers of codes that have been decoded
-    // take the same codes of the next step
-    const int lane8 = lane & 7, key = (warp - kDecodeWarp) * 8 + (lane >> 3);  // and key + 4
-    const bool swap = lane8 & 4;
+    // of keys), 8 keys per warp. A slot's codes land where its dims 64-127
+    // belong, each key's in its own row: the warp that has read its keys' codes
+    // may write their values in place
+    const int lane8 = lane & 7, key0 = (warp - kDecodeWarp) * 8, key = key0 + (lane >> 3);  // and key + 4
+    // the order of a lane's two 16-byte chunks, and of the codes behind them,
+    // that leaves no bank conflicts
+    const uint32_t swap = ((lane8 >> 2) ^ (lane >> 3)) & 1;
     const uint32_t blk = (lane8 >> 2) * 8192, c0 = 2 * (lane8 & 3);
-    const uint32_t at0 = blk + sw128_offset(key, c0 + swap), at1 = blk + sw128_offset(key, c0 + !swap);
+    const uint32_t at0 = blk + sw128_offset(key, c0 + swap), at1 = blk + sw128_offset(key, c0 + (swap ^ 1));
+    const uint32_t from = 8192 + key * 128 + 16 * lane8 + 8 * swap;  // and the other 8 codes: ^ 8
     const uint32_t full0 = in_cta(&s->full[0], even);
     Ring ring;
+    uint32_t phases = 0;  // of the slots' code barriers: q's uses of a slot do not count there
     Units u;
     bool more = c.start(p, run), ok = true;
     int kt = c.k0;
-    CodePair code[2][2];  // [key][pair of slots]
-    Rows x0{0, 0}, x1{0, 0};
-    const auto locate = [&] {
+    // the 32 scales of a step and this warp's keys, one per lane: slot lane & 3
+    // of key lane >> 2; those of the next step are in flight
+    float scale_next = 0.f;
+    const auto fetch_scales = [&] {
       if (kt == c.k0) u.start(p, c, lane, false);
       else u.advance(p, c, kt, lane, false);
-      x0 = u.of(p, c, kt, values ? 0 : a);
-      if (values) x1 = u.of(p, c, kt, 1);
-    };
-    // this lane's codes in a row `key`, and from there to the scales
-    const uint8_t* const lane_codes = p.kv + key * kF8Row + 16 * lane8 + (values ? 256 * a : 0);
-    const int to_scales = kDv - 16 * lane8 - (values ? 248 * a : 0);
-    const auto fetch = [&](int h) {
-      const Rows& x = values && h ? x1 : x0;
-      const uint8_t* row = lane_codes + static_cast<int64_t>(x.row) * kF8Row;
-      const uint8_t* scales = row + to_scales;
-      if (!values) {
-        row += 256 * h;
-        scales += 8 * h;
+      Rows x = u.of(p, c, kt, values ? 0 : a);
+      if (values) {
+        const Rows x1 = u.of(p, c, kt, 1);
+        if (lane & 2) x = x1;
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        code[i][h] = fetch_pair(row + 4 * i * kF8Row, scales + 4 * i * kF8Row, key + 4 * i < x.n);
+      const int k = key0 + (lane >> 2), group = values ? 2 * a + (lane & 1) : lane & 3;
+      scale_next = 0.f;
+      if (k < x.n)
+        asm volatile("ld.global.nc.f32 %0, [%1];"
+                     : "=f"(scale_next)
+                     : "l"(p.kv + static_cast<int64_t>(x.row + k) * kF8Row + kDv + 4 * group));
     };
-    if (more) {
-      locate();
-      fetch(0);
-      fetch(1);
-    }
+    if (more) fetch_scales();
     while (more && ok) {
       if (!values && kt == c.k0) ring.next(8);  // q's slots
+      const int left = c.req.kv_len - kt * kTile - key;  // keys that exist: behind them may lie anything
+      const float scales = scale_next;
       if (++kt == c.k1) {
         more = c.next(p);
         kt = c.k0;
       }
-      if (more) locate();
-      else x0.n = x1.n = 0;
+      if (more) fetch_scales();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int slot[2];
+      for (int h = 0; h < 2; ++h) {  // two slots at a time
+        const int n = left - 64 * (values ? h : a);
+        int to[2];
+        uint2 code[2][2][2];  // [slot][key][chunk]
 #pragma unroll
         for (int g = 0; g < 2; ++g, ring.next()) {
-          slot[g] = ring.slot;
-          ok = ok && (ring.turn == 0 || warp_wait(&s->empty[ring.slot], (ring.turn - 1) & 1));
-        }
-        if (!ok) break;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint8_t* dst = smem + slot[g] * kSlot;
+          to[g] = ring.slot;
+          ok = ok && warp_wait(&s->codes[ring.slot], (phases >> ring.slot) & 1);
+          phases ^= 1u << ring.slot;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const Decoded v = decode16(code[i][h], g, swap);
-            *reinterpret_cast<uint4*>(dst + (i ? (at0 + 512) ^ 64 : at0)) = v.first;
-            *reinterpret_cast<uint4*>(dst + (i ? (at1 + 512) ^ 64 : at1)) = v.second;
+            const uint8_t* at = smem + to[g] * kSlot + 512 * i;
+            code[g][i][0] = *reinterpret_cast<const uint2*>(at + from);
+            code[g][i][1] = *reinterpret_cast<const uint2*>(at + (from ^ 8));
           }
         }
-        fetch(h);
+        if (!ok) break;
+        __syncwarp();
+        if (__any_sync(0xFFFFFFFFu, n < 5)) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (4 * i >= n) code[g][i][0] = code[g][i][1] = make_uint2(0u, 0u);
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint8_t* dst = smem + to[g] * kSlot;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float sc = __shfl_sync(0xFFFFFFFFu, scales, 4 * ((lane >> 3) + 4 * i) + 2 * h + g);
+            *reinterpret_cast<uint4*>(dst + (i ? (at0 + 512) ^ 64 : at0)) = decode8(code[g][i][0], sc);
+            *reinterpret_cast<uint4*>(dst + (i ? (at1 + 512) ^ 64 : at1)) = decode8(code[g][i][1], sc);
+          }
+        }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane < 2) mbar_arrive_remote_relaxed(full0 + 8 * (lane ? slot[1] : slot[0]));
+        if (lane < 2) mbar_arrive_remote_relaxed(full0 + 8 * (lane ? to[1] : to[0]));
       }
     }
     if (!ok && lane == 0) abort_now();
@@ -308,7 +329,7 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
     // ---------------- all keys of each step, the own value dims
     Ring ring;
     bool ok = true;
-    for (bool more = !F8 && c.start(p, run); more && ok; more = c.next(p)) {
+    for (bool more = c.start(p, run); more && ok; more = c.next(p)) {
       Units u;
       u.start(p, c, lane, false);
       for (int kt = c.k0; kt < c.k1 && ok; ++kt) {
@@ -318,6 +339,10 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
             if (lane == 0) abort_now();
             ok = false;
             break;
+          }
+          if constexpr (F8) {
+            load_codes(ring.slot, 2 * a + (k & 1), k < 2 ? x0.row : x1.row);
+            continue;
           }
           if (a == 0 && lane == 0) mbar_arrive_expect_tx(&s->full[ring.slot], 2 * kSlot);
           load_keys(smem_u32(smem + ring.slot * kSlot), &maps.keys, &maps.row, in_cta(&s->full[ring.slot], even),
@@ -736,14 +761,15 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
 template <bool F8>
 __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const __grid_constant__ DenseParams p,
                                                                           const __grid_constant__ Maps quad_maps,
-                                                                          const __grid_constant__ Maps pair_maps) {
+                                                                          const __grid_constant__ Maps pair_maps,
+                                                                          const __grid_constant__ CodeMaps code_maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   if (misaligned(p, smem)) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Run* run = reinterpret_cast<const Run*>(smem + kSmRun);
   plan_run<kThreadsOf<F8>, kQuad>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);
   if (run->kind == kQuad) {
-    run_quad<F8>(p, quad_maps, smem);
+    run_quad<F8>(p, quad_maps, code_maps, smem);
   } else {
     pairs::set_up<F8>(reinterpret_cast<pairs::Bars*>(smem + pairs::kSmBar), pair_maps);
     pairs::run_pair<F8>(p, pair_maps, smem);
@@ -788,14 +814,16 @@ int clusters_at_once() {
 template <bool F8>
 dsa_status_t launch(const DenseParams& p, const void* q, const void* kv, cudaStream_t s) {
   Maps quad_maps, pair_maps;
+  CodeMaps code_maps = {};
   dsa_status_t st;
   if ((st = make_maps(&quad_maps, p, F8, q, kv, 128, 1)) != DSA_OK) return st;
   if ((st = make_maps(&pair_maps, p, F8, q, kv, 64, 9)) != DSA_OK) return st;
+  if (F8 && (st = make_code_maps(&code_maps, p, kv)) != DSA_OK) return st;
   if ((st = allow_smem(dense_mla_quad_kernel<F8>, kSmTotal, g_smem[F8])) != DSA_OK) return st;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   config<F8>(&cfg, attr, p.quads, s);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_quad_kernel<F8>, p, quad_maps, pair_maps);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_quad_kernel<F8>, p, quad_maps, pair_maps, code_maps);
   if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_quad_kernel launch failed: %s", cudaGetErrorString(e));
   return DSA_OK;
 }

@@ -27,8 +27,9 @@ namespace dsa {
 namespace dense {
 namespace {
 
-// warps 0-3 softmax and results, 4 loads, 5 MMA
-constexpr int kLoadWarp = 4, kMmaWarp = 5, kThreads = 192;
+// warps 0-3 softmax and results, 4 loads, 5 MMA; fp8 cache: 6-13 decode
+constexpr int kLoadWarp = 4, kMmaWarp = 5, kDecodeWarp = 6, kDecodeWarps = 8;
+constexpr int threads(bool f8) { return 32 * (kDecodeWarp + (f8 ? kDecodeWarps : 0)); }
 constexpr int kRing = 5, kPairSlot = 32768;  // slots of 128 keys x 128 dims (two blocks of 64), four per step
 
 template <int N>
@@ -36,7 +37,8 @@ struct Layout {
   static constexpr int kRopes = N == 16 ? 2 : 1;  // buffers of 128 keys x 64 rope dims
   static constexpr int kRope = kRing * kPairSlot, kQ = kRope + kRopes * 16384;
   static constexpr int kP = kQ + 9 * N * 128;  // q as 9 blocks of N rows x 64 dims; P: 2 blocks of N rows x 64 keys
-  static constexpr int kRed = kP + 2 * N * 128, kLim = kRed + 2 * 4 * N * 4, kBar = kLim + N * 4;
+  static constexpr int kRed = kP + 2 * N * 128, kLim = kRed + 2 * 4 * N * 4,
+                       kScales = kLim + 128, kBar = kScales + 4096;
   static constexpr uint32_t kColS = 0, kColO = 2 * N, kTmemCols = N == 16 ? 128 : 256;  // S 2 x N, O 4 x N
   static_assert(kBar + 256 <= kSmRun, "shared memory");
 };
@@ -45,6 +47,7 @@ struct Bars {
   uint64_t full[kRing], empty[kRing], rope_full[2], rope_empty[2];
   uint64_t q_full, q_free;  // q_free: the row tile's last S has read q
   uint64_t s_full[2], p_full, pv_done[2], meet;
+  uint64_t codes[kRing];  // fp8: a slot's codes landed
   uint32_t tmem;
   volatile int abort;
 };
@@ -79,9 +82,10 @@ __device__ __forceinline__ void load_blocks(uint32_t dst, const Maps& maps, uint
   __syncwarp();
 }
 
-template <int N>
-__global__ void __launch_bounds__(kThreads, 1) dense_mla_rows_kernel(const __grid_constant__ DenseParams p,
-                                                                     const __grid_constant__ Maps maps) {
+template <int N, bool F8>
+__global__ void __launch_bounds__(threads(F8), 1) dense_mla_rows_kernel(const __grid_constant__ DenseParams p,
+                                                                       const __grid_constant__ Maps maps,
+                                                                       const __grid_constant__ CodeMaps code_maps) {
   using L = Layout<N>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (misaligned(p, smem)) return;
@@ -90,8 +94,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_rows_kernel(const __gri
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&s->full[i], 1);
+      mbar_init(&s->full[i], F8 ? kDecodeWarps : 1);
       mbar_init(&s->empty[i], 1);
+      mbar_init(&s->codes[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s->rope_full[i], 1);
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_rows_kernel(const __gri
   tc_fence_after();
   const uint32_t tmem = s->tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_run<kThreads, kSingle>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);
+  plan_run<threads(F8), kSingle>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);
 
   const auto abort_now = [&] {
     s->abort = 1;
@@ -130,8 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_rows_kernel(const __gri
   bool ok = true;
 
   if (warp == kLoadWarp) {
-    // ---------------- q of each row tile, and the keys: per step four slots
-    // of 128 dims, then the rope dims
+    // ---------------- q of each row tile, and the keys: per step the rope dims,
+    // then four slots of 128 dims (fp8: their codes)
     int slot = 0, it = 0, seg = 0;
     uint32_t turn = 0;
     for (bool more = c.start(p, run); more && ok; more = c.next(p), ++seg) {
@@ -151,11 +156,30 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_rows_kernel(const __gri
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&s->rope_full[rb], 16384);
         __syncwarp();
-        load_blocks<1>(smem_u32(smem + L::kRope + rb * 16384), maps, &s->rope_full[rb], x0, x1, p.total_rows, 8, lane);
+        load_blocks<1>(smem_u32(smem + L::kRope + rb * 16384), maps, &s->rope_full[rb], x0, x1, p.total_rows, F8 ? 0 : 8,
+                       lane);
         for (int k = 0; k < 4; ++k) {
           if (turn > 0 && !warp_wait(&s->empty[slot], (turn - 1) & 1)) {
             ok = false;
             break;
+          }
+          if constexpr (F8) {
+            // the codes to where their own keys' dims 64-127 will be
+            if (lane == 0) mbar_arrive_expect_tx(&s->codes[slot], 16384 + (k == 0 ? 2048 : 0));
+            __syncwarp();
+            const int row = (lane & 1) ? x1.row : x0.row;
+            if (lane < 2)
+              tma_load_2d(smem_u32(smem + slot * kPairSlot + 16384 + lane * 8192), &code_maps.codes, &s->codes[slot],
+                          128 * k, row);
+            else if (k == 0 && lane < 4)
+              tma_load_2d(smem_u32(smem + L::kScales + (it & 1) * 2048 + (lane & 1) * 1024), &code_maps.scales,
+                          &s->codes[slot], kDv, row);
+            __syncwarp();
+            if (++slot == kRing) {
+              slot = 0;
+              ++turn;
+            }
+            continue;
           }
           if (lane == 0) mbar_arrive_expect_tx(&s->full[slot], kPairSlot);
           __syncwarp();
@@ -169,6 +193,63 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_rows_kernel(const __gri
     }
     if (!ok && lane == 0) abort_now();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else if (F8 && warp >= kDecodeWarp) {
+    // ---------------- fp8: a step's four slots, 16 keys per warp. A slot's codes
+    // land where its dims 64-127 belong, each key's in its own row: the warp that
+    // has read its keys' codes may write their values in place
+    const int w = warp - kDecodeWarp, lane8 = lane & 7, key = w * 16 + (lane >> 3);  // and key + 4, 8, 12
+    // the order of a lane's two 16-byte chunks, and of the codes behind them,
+    // that leaves no bank conflicts
+    const uint32_t swap = ((lane8 >> 2) ^ (lane >> 3)) & 1;
+    const uint32_t blk = (lane8 >> 2) * 16384, c0 = 2 * (lane8 & 3);
+    const uint32_t at0 = blk + sw128_offset(key, c0 + swap), at1 = blk + sw128_offset(key, c0 + (swap ^ 1));
+    const uint32_t from = 16384 + key * 128 + 16 * lane8 + 8 * swap;  // and the other 8 codes: ^ 8
+    int slot = 0, it = 0;
+    uint32_t turn = 0;
+    for (bool more = c.start(p, run); more && ok; more = c.next(p)) {
+      for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
+        // keys of this warp that exist: behind them may lie anything
+        const int n = c.req.kv_len - kt * kTile - w * 16 - (lane >> 3);
+        const uint8_t* scales = smem + L::kScales + (it & 1) * 2048 + key * 16;
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          ok = warp_wait(&s->codes[slot], turn & 1);
+          if (!ok) break;
+          uint8_t* dst = smem + slot * kPairSlot;
+          uint2 code[4][2];
+          float sc[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            code[i][0] = *reinterpret_cast<const uint2*>(dst + 512 * i + from);
+            code[i][1] = *reinterpret_cast<const uint2*>(dst + 512 * i + (from ^ 8));
+            sc[i] = *reinterpret_cast<const float*>(scales + 64 * i + 4 * g);
+          }
+          __syncwarp();
+          if (__any_sync(0xFFFFFFFFu, n < 13)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (4 * i < n) continue;
+              code[i][0] = code[i][1] = make_uint2(0u, 0u);
+              sc[i] = 0.f;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t up = (i >> 1) * 1024;
+            *reinterpret_cast<uint4*>(dst + up + ((i & 1) ? (at0 + 512) ^ 64 : at0)) = decode8(code[i][0], sc[i]);
+            *reinterpret_cast<uint4*>(dst + up + ((i & 1) ? (at1 + 512) ^ 64 : at1)) = decode8(code[i][1], sc[i]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s->full[slot]);
+          if (++slot == kRing) {
+            slot = 0;
+            ++turn;
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) abort_now();
   } else if (warp == kMmaWarp) {
     // ---------------- MMA: whatever is ready, PV of the oldest step first. The
     // warp stays converged, so that the descriptors live in uniform registers;
@@ -261,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_rows_kernel(const __gri
       if (progressed) idle_since = clock64();
       else if (all(clock64() - idle_since > kWaitLimitCycles) && lane == 0) abort_now();
     }
-  } else {
+  } else if (warp < kLoadWarp) {
     // ---------------- softmax: TMEM lane = key (then, of O^T, dim), columns = rows
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     float* red = reinterpret_cast<float*>(smem + L::kRed);  // [step parity][warp][row]
@@ -456,17 +537,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_mla_rows_kernel(const __gri
   if (warp == kMmaWarp) tmem_dealloc(tmem, L::kTmemCols);
 }
 
-FuncAttrOnce g_smem[2];
+FuncAttrOnce g_smem[3];
 
-template <int N>
+template <int N, bool F8>
 dsa_status_t launch(const DenseParams& p, const void* q, const void* kv, cudaStream_t s) {
   Maps maps;
-  dsa_status_t st = make_maps(&maps, p, false, q, kv, N, 9);
+  CodeMaps code_maps = {};
+  dsa_status_t st = make_maps(&maps, p, F8, q, kv, N, 9);
+  if (st == DSA_OK && F8) st = make_code_maps(&code_maps, p, kv);
   if (st != DSA_OK) return st;
-  if ((st = allow_smem(dense_mla_rows_kernel<N>, kSmTotal, g_smem[N == 32])) != DSA_OK) return st;
+  if ((st = allow_smem(dense_mla_rows_kernel<N, F8>, kSmTotal, g_smem[F8 ? 2 : N == 32])) != DSA_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.singles));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads(F8));
   cfg.dynamicSmemBytes = kSmTotal;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -474,7 +557,7 @@ dsa_status_t launch(const DenseParams& p, const void* q, const void* kv, cudaStr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_rows_kernel<N>, p, maps);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_rows_kernel<N, F8>, p, maps, code_maps);
   if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_rows_kernel launch failed: %s", cudaGetErrorString(e));
   return DSA_OK;
 }
@@ -485,14 +568,15 @@ dsa_status_t launch(const DenseParams& p, const void* q, const void* kv, cudaStr
 // at a time. Against pairs (us, from a graph, caches cold): 64 requests of 4096
 // keys and 32 heads 90 and 95; 128 of 1000 and 8 heads 52 and 69; 8 of 8192 and
 // 16 heads 40 and 48; one of 1000 keys 20 and 30; one of 64 keys 21.6 and 20.
-int single_rows(int32_t B, int32_t T, int32_t H) {
-  for (int n = 16; n <= 32; n *= 2)
+int single_rows(int32_t B, int32_t T, int32_t H, bool f8) {
+  for (int n = 16; n <= (f8 ? 16 : 32); n *= 2)
     if (H <= n && static_cast<int64_t>(T) * H <= static_cast<int64_t>(n) * B) return n;
   return 0;
 }
 
-dsa_status_t launch_singles(const DenseParams& p, const void* q, const void* kv, cudaStream_t s) {
-  return p.single_rows == 16 ? launch<16>(p, q, kv, s) : launch<32>(p, q, kv, s);
+dsa_status_t launch_singles(const DenseParams& p, bool f8, const void* q, const void* kv, cudaStream_t s) {
+  if (f8) return launch<16, true>(p, q, kv, s);
+  return p.single_rows == 16 ? launch<16, false>(p, q, kv, s) : launch<32, false>(p, q, kv, s);
 }
 
 }  // namespace dense

@@ -138,16 +138,18 @@ FEW_CASES = {
 }
 
 
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("name", sorted(FEW_CASES))
-def test_few_rows(name):
+def test_few_rows(name, fp8):
     lens, q_lens, H, block = FEW_CASES[name]
-    check(make_dense_case(lens, q_lens, H, block=block, seed=len(name)))
+    check(make_dense_case(lens, q_lens, H, fp8=fp8, block=block, seed=len(name)))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("H", [16, 32])
 @pytest.mark.parametrize("q_std", [0.0, 300.0])
-def test_few_rows_score_ranges(H, q_std):
-    check(make_dense_case([7000, 5000, 90], [1, 1, 1], H, q_std=q_std, seed=41))
+def test_few_rows_score_ranges(H, q_std, fp8):
+    check(make_dense_case([7000, 5000, 90], [1, 1, 1], H, fp8=fp8, q_std=q_std, seed=41))
 
 
 @pytest.mark.parametrize("H", [16, 32])
@@ -163,8 +165,9 @@ def test_few_rows_rising_scores(H):
     check(c)
 
 
-def test_few_rows_with_bad_blocks_and_lengths():
-    c = make_dense_case([6000, 1, 7000], [1, 2, 1], 16, seed=43, pad_tokens=3, extra_rows=8, extra_cols=2)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_few_rows_with_bad_blocks_and_lengths(fp8):
+    c = make_dense_case([6000, 1, 7000], [1, 2, 1], 16, fp8=fp8, seed=43, pad_tokens=3, extra_rows=8, extra_cols=2)
     for b, j, v in ((0, 1, 10 ** 6), (0, 93, -5), (2, 40, int(c["cache"].shape[0])), (2, 109, -1)):
         c["table"][b, j] = v
     out, lse = check(c, status=api.DSA_DEVERR_BLOCK_OOB | api.DSA_DEVERR_SEQ_LEN,
