@@ -109,13 +109,14 @@ __global__ void __launch_bounds__(128) dense_mla_merge_kernel(const __grid_const
 
 template <bool F8>
 __global__ void __launch_bounds__(pairs::threads(F8), 1) dense_mla_kernel(const __grid_constant__ DenseParams p,
-                                                                          const __grid_constant__ Maps maps) {
+                                                                          const __grid_constant__ Maps maps,
+                                                                          const __grid_constant__ CodeMaps code_maps) {
   extern __shared__ __align__(1024) uint8_t smem[];
   if (misaligned(p, smem)) return;
   pairs::set_up<F8>(reinterpret_cast<pairs::Bars*>(smem + pairs::kSmBar), maps);  // overlaps the kernel before
   asm volatile("griddepcontrol.wait;" ::: "memory");
   plan_run<pairs::threads(F8), kPair>(p, reinterpret_cast<Run*>(smem + kSmRun), smem);
-  pairs::run_pair<F8>(p, maps, smem);
+  pairs::run_pair<F8>(p, maps, code_maps, smem);
 }
 
 FuncAttrOnce g_smem_dense[2], g_smem_merge;
@@ -130,7 +131,9 @@ size_t workspace_bytes(int pairs) { return o_part_bytes(pairs) + ml_part_bytes(p
 template <bool F8>
 dsa_status_t launch_pairs(const DenseParams& p, const void* q, const void* kv, cudaStream_t s) {
   Maps maps;
+  CodeMaps code_maps = {};
   dsa_status_t st = make_maps(&maps, p, F8, q, kv, 64, 9);
+  if (st == DSA_OK && F8) st = make_code_maps(&code_maps, p, kv);
   if (st != DSA_OK) return st;
   if ((st = allow_smem(dense_mla_kernel<F8>, kSmTotal, g_smem_dense[F8])) != DSA_OK) return st;
   cudaLaunchConfig_t cfg = {};
@@ -147,7 +150,7 @@ dsa_status_t launch_pairs(const DenseParams& p, const void* q, const void* kv, c
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_kernel<F8>, p, maps);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, dense_mla_kernel<F8>, p, maps, code_maps);
   if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "dense_mla_kernel launch failed: %s", cudaGetErrorString(e));
   return DSA_OK;
 }

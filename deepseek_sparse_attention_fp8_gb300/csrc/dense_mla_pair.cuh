@@ -39,10 +39,11 @@ namespace pairs {
 
 // Warps 0-7 softmax, 8 q / rope (bf16 cache: and the other keys), 9 MMA, then
 // the own keys: one warp of TMA copies, or (fp8 cache) 8 decoding warps, which
-// take the other keys too. Nothing may spill: beside 227 KB of shared memory
+// take the other keys too, and one that copies codes. Nothing may spill: beside 227 KB of shared memory
 // the L1 is so small that spilled registers come back from L2.
 constexpr int kAuxWarp = 8, kMmaWarp = 9, kKeyWarp = 10, kDecodeWarps = 8;
-constexpr int threads(bool f8) { return 32 * (kKeyWarp + (f8 ? kDecodeWarps : 1)); }
+constexpr int kCodeWarp = kKeyWarp + kDecodeWarps;
+constexpr int threads(bool f8) { return 32 * (kKeyWarp + (f8 ? kDecodeWarps + 1 : 1)); }
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;  // O 256 columns, S 2 x 64
 
 // Shared memory: q as 9 blocks of 64 rows x 64 dims, two steps of 4 key slots,
@@ -62,6 +63,7 @@ struct Bars {
   uint64_t pv_half[2];   // the first 64 keys of a step have entered O (in both CTAs)
   uint64_t pv_done[2];   // O += P V of a step complete (in both CTAs)
   uint64_t rows[2];      // the four softmax warps that share 32 rows
+  uint64_t codes[2][4], other_codes[2][2];  // fp8: a slot's codes landed
   uint64_t first;        // q and the rope dims of the run's first step have been asked for
   uint32_t tmem;
   volatile int abort;
@@ -76,6 +78,8 @@ __device__ __forceinline__ void set_up(Bars* s, const Maps& maps) {
     for (int i = 0; i < 2; ++i) {
       for (int k = 0; k < 4; ++k) mbar_init(&s->full[i][k], F8 ? 2 * kDecodeWarps : 1);
       for (int k = 0; k < 2; ++k) mbar_init(&s->other[i][k], F8 ? kDecodeWarps : 1);
+      for (int k = 0; k < 4; ++k) mbar_init(&s->codes[i][k], 1);
+      for (int k = 0; k < 2; ++k) mbar_init(&s->other_codes[i][k], 1);
       mbar_init(&s->s_half[i], 1);
       mbar_init(&s->pv_half[i], 1);
       mbar_init(&s->s_full[i], 1);
@@ -107,7 +111,8 @@ __device__ __forceinline__ void set_up(Bars* s, const Maps& maps) {
 // Works on this pair's run, and ends with a cluster barrier. A pair is cluster
 // ranks 2 n and 2 n + 1.
 template <bool F8>
-__device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps, uint8_t* smem) {
+__device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps, const CodeMaps& code_maps,
+                                         uint8_t* smem) {
   Bars* s = reinterpret_cast<Bars*>(smem + kSmBar);
   const Run* run = reinterpret_cast<const Run*>(smem + kSmRun);
   float* red = reinterpret_cast<float*>(smem + kSmRed);
@@ -120,94 +125,117 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
     s->abort = 1;
     report(p.dev_status, DSA_DEVERR_TIMEOUT);
   };
+  // fp8: 64 keys' codes of a group, to where their dims 64-127 will be
+  const auto load_codes = [&](uint64_t* bar, int slot, int group, int row) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, 8192);
+      tma_load_2d(smem_u32(smem + kSmKv + slot * kSlot + 8192), &code_maps.codes, bar, 128 * group, row);
+    }
+    __syncwarp();
+  };
   // a barrier's address in the even CTA
   const auto even = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), base); };
 
   if (F8 && warp >= kKeyWarp && warp < kKeyWarp + kDecodeWarps) {
     // ---------------- fp8: the own keys of each step, 8 per warp, two groups
-    // (slots) at a time, the next two in flight; then the other keys of the
-    // step before, as soon as S no longer needs the dims they replace
-    const int lane8 = lane & 7, key = (warp - kKeyWarp) * 8 + (lane >> 3);  // and key + 4
-    const bool swap = lane8 & 4;
-    // the two chunks of key (key + 4: 4 rows of 128 bytes further, chunk bit 2 flipped)
+    // (slots) at a time, then the other keys of the step before. A slot's codes
+    // land where its dims 64-127 belong, each key's in its own row: the warp that
+    // has read its keys' codes may write their values in place
+    const int lane8 = lane & 7, key0 = (warp - kKeyWarp) * 8, key = key0 + (lane >> 3);  // and key + 4
+    // the order of a lane's two 16-byte chunks, and of the codes behind them,
+    // that leaves no bank conflicts
+    const uint32_t swap = ((lane8 >> 2) ^ (lane >> 3)) & 1;
     const uint32_t blk = (lane8 >> 2) * 8192, c0 = 2 * (lane8 & 3);
-    const uint32_t at0 = blk + sw128_offset(key, c0 + swap), at1 = blk + sw128_offset(key, c0 + !swap);
-    const auto store = [&](uint8_t* slot, int i, const Decoded& v) {
-      *reinterpret_cast<uint4*>(slot + (i ? (at0 + 512) ^ 64 : at0)) = v.first;
-      *reinterpret_cast<uint4*>(slot + (i ? (at1 + 512) ^ 64 : at1)) = v.second;
+    const uint32_t at0 = blk + sw128_offset(key, c0 + swap), at1 = blk + sw128_offset(key, c0 + (swap ^ 1));
+    const uint32_t from = 8192 + key * 128 + 16 * lane8 + 8 * swap;  // and the other 8 codes: ^ 8
+    // two slots; scales: this warp's, of key k and the slot's group in lane
+    // 4 k + sc0 (+ 1); keys from n on do not exist (behind them may lie anything)
+    const auto decode = [&](uint8_t* slot, float scales, int sc0, int n) {
+      uint2 code[2][2][2];  // [slot][key][chunk]
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* at = slot + g * kSlot + 512 * i;
+          code[g][i][0] = *reinterpret_cast<const uint2*>(at + from);
+          code[g][i][1] = *reinterpret_cast<const uint2*>(at + (from ^ 8));
+        }
+      }
+      __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, n < 5)) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (4 * i >= n) code[g][i][0] = code[g][i][1] = make_uint2(0u, 0u);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint8_t* dst = slot + g * kSlot;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float sc = __shfl_sync(0xFFFFFFFFu, scales, 4 * ((lane >> 3) + 4 * i) + sc0 + g);
+          *reinterpret_cast<uint4*>(dst + (i ? (at0 + 512) ^ 64 : at0)) = decode8(code[g][i][0], sc);
+          *reinterpret_cast<uint4*>(dst + (i ? (at1 + 512) ^ 64 : at1)) = decode8(code[g][i][1], sc);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
     };
     Cursor<kPair> c;
     bool more = c.start(p, run), ok = true;
     int kt = c.k0;
-    CodePair own[2], oth[2];  // [key]
-    Rows x{0, 0}, xo{0, 0};
     Units u;
-    const bool rep = warp == kKeyWarp && r == 0;
-    const auto locate = [&] {
-      if (kt == c.k0) u.start(p, c, lane, rep);
-      const Rows a = u.get(p, c, 2 * kt, lane, rep), b = u.get(p, c, 2 * kt + 1, lane, rep);
-      x = r ? b : a;
-      xo = r ? a : b;
+    float own_next = 0.f, other_next = 0.f;  // scales of the next step
+    const auto scale_of = [&](Rows x, int group) {
+      float v = 0.f;
+      const int k = key0 + (lane >> 2);
+      if (k < x.n)
+        asm volatile("ld.global.nc.f32 %0, [%1];"
+                     : "=f"(v)
+                     : "l"(p.kv + static_cast<int64_t>(x.row + k) * kF8Row + kDv + 4 * group));
+      return v;
     };
-    const auto fetch_own = [&](int h) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint8_t* row = p.kv + static_cast<int64_t>(x.row + key + 4 * i) * kF8Row;
-        own[i] = fetch_pair(row + 256 * h + 16 * lane8, row + kDv + 8 * h, key + 4 * i < x.n);
-      }
+    const auto fetch_scales = [&] {
+      if (kt == c.k0) u.start(p, c, lane, false);
+      else u.advance(p, c, kt, lane, false);
+      own_next = scale_of(u.of(p, c, kt, r), lane & 3);
+      other_next = scale_of(u.of(p, c, kt, r ^ 1), 2 * r + (lane & 1));
     };
-    const auto fetch_other = [&](const Rows& xo) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint8_t* row = p.kv + static_cast<int64_t>(xo.row + key + 4 * i) * kF8Row;
-        oth[i] = fetch_pair(row + 256 * r + 16 * lane8, row + kDv + 8 * r, key + 4 * i < xo.n);
-      }
-    };
-    if (more) {
-      locate();
-      fetch_own(0);
-    }
+    if (more) fetch_scales();
     const auto all = [](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
+    float other_scales = 0.f;
+    int other_n = 0;
     for (int it = 0; ok && (more || it > 0); ++it) {
       const int buf = it & 1, b1 = buf ^ 1;
       const bool last = !more;  // only the other keys of the last step are left
-      const Rows xo_now = xo;
+      const float own_scales = own_next, old_scales = other_scales;
+      const int left = c.req.kv_len - kt * kTile - key, old_n = other_n;
+      other_scales = other_next;
+      other_n = left - 64 * (r ^ 1);
+      if (!last) {
+        if (++kt == c.k1) {
+          more = c.next(p);
+          kt = c.k0;
+        }
+        if (more) fetch_scales();
+      }
       int h = last ? 2 : 0;
       bool other_left = it > 0;
       long long idle_since = clock64();
 #pragma unroll 1
-      while (h < 2 || other_left) {  // whichever may be stored; the other keys are waited for more urgently
-        if (other_left && all(mbar_test_wait(r ? &s->s_half[b1] : &s->s_full[b1], ((it - 1) >> 1) & 1))) {
-          uint8_t* slot = smem + kSmKv + (b1 * 4 + 2 * (r ^ 1)) * kSlot;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(oth[i].c[g], g ? oth[i].sc.y : oth[i].sc.x, swap));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+      while (h < 2 || other_left) {  // whichever has landed; the other keys are waited for more urgently
+        if (other_left && all(mbar_test_wait(&s->other_codes[b1][0], ((it - 1) >> 1) & 1) &&
+                              mbar_test_wait(&s->other_codes[b1][1], ((it - 1) >> 1) & 1))) {
+          decode(smem + kSmKv + (b1 * 4 + 2 * (r ^ 1)) * kSlot, old_scales, 0, old_n);
           if (lane == 0) mbar_arrive_remote_relaxed(even(&s->other[b1][r ^ 1]));
           other_left = false;
-        } else if (h < 2 && (it < 2 || all(mbar_test_wait(h == 0 ? &s->pv_half[buf] : &s->pv_done[buf],
-                                                          ((it >> 1) - 1) & 1)))) {
-          uint8_t* slot = smem + kSmKv + (buf * 4 + 2 * h) * kSlot;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) store(slot + g * kSlot, i, decode16(own[i].c[g], g ? own[i].sc.y : own[i].sc.x, swap));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+        } else if (h < 2 && all(mbar_test_wait(&s->codes[buf][2 * h], (it >> 1) & 1) &&
+                                mbar_test_wait(&s->codes[buf][2 * h + 1], (it >> 1) & 1))) {
+          decode(smem + kSmKv + (buf * 4 + 2 * h) * kSlot, own_scales, 2 * h, left - 64 * r);
           if (lane < 2) mbar_arrive_remote_relaxed(even(&s->full[buf][2 * h + lane]));
           ++h;
-          if (h == 2) {
-            if (++kt == c.k1) {
-              more = c.next(p);
-              kt = c.k0;
-            }
-            if (more) locate();
-          }
-          if (h == 1 || more) fetch_own(h & 1);
         } else if (all(clock64() - idle_since > kWaitLimitCycles)) {
           if (lane == 0) abort_now();
           ok = false;
@@ -215,7 +243,27 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
         }
       }
       if (last) break;
-      fetch_other(xo_now);
+    }
+  } else if (F8 && warp == kCodeWarp) {
+    // ---------------- fp8: the codes of each step's own keys
+    Cursor<kPair> c;
+    int it = 0;
+    bool ok = true;
+    for (bool more = c.start(p, run); more && ok; more = c.next(p)) {
+      Units u;
+      u.start(p, c, lane, true);
+      for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
+        const int buf = it & 1;
+        const Rows x = u.get(p, c, 2 * kt + r, lane, true);
+        for (int k = 0; k < 4; ++k) {
+          if (it >= 2 && (k & 1) == 0 && !warp_wait(k == 0 ? &s->pv_half[buf] : &s->pv_done[buf], ((it >> 1) - 1) & 1)) {
+            if (lane == 0) abort_now();
+            ok = false;
+            break;
+          }
+          load_codes(&s->codes[buf][k], buf * 4 + k, k, x.row);
+        }
+      }
     }
   } else if (!F8 && warp == kKeyWarp) {
     // ---------------- the own keys of each step, all 512 latent dims
@@ -249,7 +297,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
       }
     }
   } else if (warp == kAuxWarp) {
-    // ---------------- each step's other keys (bf16 cache), as soon as S no
+    // ---------------- each step's other keys (fp8: their codes), as soon as S no
     // longer needs the dims they replace (CTA 1: after the first two slots,
     // CTA 0: after all), the rope dims of the next step's own keys, and q when
     // a row tile begins
@@ -258,6 +306,10 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
     Rows other{0, 0};
     const auto load_other = [&](int i) {
       const int buf = i & 1;
+      if constexpr (F8) {
+        for (int k = 0; k < 2; ++k) load_codes(&s->other_codes[buf][k], buf * 4 + 2 * (r ^ 1) + k, 2 * r + k, other.row);
+        return;
+      }
       if (r == 0 && lane == 0) {
         mbar_arrive_expect_tx(&s->other[buf][0], 2 * kSlot);
         mbar_arrive_expect_tx(&s->other[buf][1], 2 * kSlot);
@@ -270,7 +322,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
     bool ok = true;
     const auto after_s = [&](int i) {  // what follows S of step i; false when a wait ran out
       const int ph = (i >> 1) & 1;
-      if (!F8 && r == 1) {
+      if (r == 1) {
         ok = warp_wait(&s->s_half[i & 1], ph);
         if (ok) load_other(i);
       }
@@ -307,12 +359,12 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
         load_keys(smem_u32(smem + kSmRope), &maps.rope, &maps.row, even(&s->rope), x, p.total_rows, F8 ? 0 : 8, 1,
                   lane);
         if (!F8 && it == 0 && lane == 0) mbar_arrive(&s->first);
-        if (!F8 && it >= 1 && r == 0) load_other(it - 1);
+        if (it >= 1 && r == 0) load_other(it - 1);
         if (it >= 1 && kt == c.k0) load_q(row0);
         other = next_other;
       }
     }
-    if (!F8 && ok && it >= 1 && after_s(it - 1) && r == 0) load_other(it - 1);
+    if (ok && it >= 1 && after_s(it - 1) && r == 0) load_other(it - 1);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   } else if (warp == kMmaWarp) {
     // ---------------- MMA: the even CTA issues for the pair whatever is

@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(kThreadsOf<F8>, 1) dense_mla_quad_kernel(const
     run_quad<F8>(p, quad_maps, code_maps, smem);
   } else {
     pairs::set_up<F8>(reinterpret_cast<pairs::Bars*>(smem + pairs::kSmBar), pair_maps);
-    pairs::run_pair<F8>(p, pair_maps, smem);
+    pairs::run_pair<F8>(p, pair_maps, code_maps, smem);
   }
 }
 
