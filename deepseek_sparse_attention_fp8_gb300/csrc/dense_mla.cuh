@@ -263,10 +263,9 @@ __device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* box, 
   __syncwarp();
 }
 
-// ---- fp8 cache: a row's 128 codes of one group are 8 lanes' 16 bytes, read
-// straight into registers, decoded (code * scale in fp32, rounded to bf16:
-// the tensor cores take bf16) and stored as the swizzled tile the copies of
-// the bf16 cache would bring.
+// ---- fp8 cache: a key's 128 codes of a group are 8 lanes' 16, decoded (code *
+// scale in fp32, rounded to bf16: the tensor cores take bf16) and stored as the
+// swizzled tile that the copies of the bf16 cache would bring.
 __device__ __forceinline__ float2 mul2(float2 a, float s) {  // two products in one instruction
   float2 r;
   asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmul.rn.f32x2 c, a, b;\n\t"
@@ -282,37 +281,73 @@ __device__ __forceinline__ uint32_t decode2(uint32_t two, float sc) {
   const float2 v = mul2(f, sc);
   return pack_bf16(v.x, v.y);
 }
-__device__ __forceinline__ uint4 decode8(uint32_t a, uint32_t b, float sc) {
-  return make_uint4(decode2(a, sc), decode2(a >> 16, sc), decode2(b, sc), decode2(b >> 16, sc));
+__device__ __forceinline__ uint4 decode8(uint2 c, float sc) {
+  return make_uint4(decode2(c.x, sc), decode2(c.x >> 16, sc), decode2(c.y, sc), decode2(c.y >> 16, sc));
 }
-// 16 codes (lane8: which) of each of two neighbouring groups of a key, none
-// where the key does not exist. The upper four lanes of a key write another
-// 64-dim block than the lower four, in the same banks: they store their two
-// 16-byte chunks in the other order.
-__device__ __forceinline__ uint4 decode8(uint2 c, float sc) { return decode8(c.x, c.y, sc); }
-struct CodePair {
-  uint4 c[2];
-  float2 sc;
-};
-__device__ __forceinline__ CodePair fetch_pair(const uint8_t* codes, const uint8_t* scales, bool exists) {
-  CodePair v{{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, make_float2(0.f, 0.f)};
-  if (exists) {
-    // volatile: issued here, ahead of the waits, not where the values are used
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v.c[g].x), "=r"(v.c[g].y), "=r"(v.c[g].z), "=r"(v.c[g].w)
-                   : "l"(codes + 128 * g));
-    asm volatile("ld.global.nc.v2.f32 {%0, %1}, [%2];" : "=f"(v.sc.x), "=f"(v.sc.y) : "l"(scales));
+
+// A decoding warp's part, 8 keys from key0 on, of slots of 64 keys x 128 dims.
+// A slot's codes land where its dims 64-127 belong, each key's in its own row:
+// the warp that has read its keys' codes may write their values in place.
+struct Decoder {
+  int key0;
+  uint32_t at0, at1, from;
+  __device__ __forceinline__ Decoder(int w, int lane) {
+    const int lane8 = lane & 7, key = 8 * w + (lane >> 3);  // and key + 4
+    // the order of a lane's two 16-byte chunks, and of the codes behind them,
+    // that leaves no bank conflicts
+    const uint32_t swap = ((lane8 >> 2) ^ (lane >> 3)) & 1;
+    const uint32_t blk = (lane8 >> 2) * 8192, c0 = 2 * (lane8 & 3);
+    key0 = 8 * w;
+    at0 = blk + sw128_offset(key, c0 + swap);
+    at1 = blk + sw128_offset(key, c0 + (swap ^ 1));
+    from = 8192 + key * 128 + 16 * lane8 + 8 * swap;  // and the other 8 codes: ^ 8
   }
-  return v;
-}
-struct Decoded {
-  uint4 first, second;
+  // the scale of this warp's key lane >> 2
+  __device__ __forceinline__ float scale(const DenseParams& p, Rows x, int group, int lane) const {
+    float v = 0.f;
+    const int k = key0 + (lane >> 2);
+    if (k < x.n)  // volatile: issued here, a step ahead
+      asm volatile("ld.global.nc.f32 %0, [%1];"
+                   : "=f"(v)
+                   : "l"(p.kv + static_cast<int64_t>(x.row + k) * kF8Row + kDv + 4 * group));
+    return v;
+  }
+  // this lane's codes in a slot: [key][chunk]
+  __device__ __forceinline__ void read(const uint8_t* slot, uint2 (&code)[2][2]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      code[i][0] = *reinterpret_cast<const uint2*>(slot + 512 * i + from);
+      code[i][1] = *reinterpret_cast<const uint2*>(slot + 512 * i + (from ^ 8));
+    }
+  }
+  // Two slots' values, behind their codes' read; scales: key k's in lanes 4 k +
+  // sc0 and 4 k + sc0 + 1. Keys from n on (counted from this lane's first) do
+  // not exist; behind them may lie anything.
+  __device__ __forceinline__ void write(uint8_t* slot0, uint8_t* slot1, uint2 (&code)[2][2][2], float scales, int sc0,
+                                        int n, int lane) const {
+    __syncwarp();
+    if (__any_sync(0xFFFFFFFFu, n < 5)) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (4 * i >= n) code[g][i][0] = code[g][i][1] = make_uint2(0u, 0u);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint8_t* dst = g ? slot1 : slot0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float sc = __shfl_sync(0xFFFFFFFFu, scales, 4 * ((lane >> 3) + 4 * i) + sc0 + g);
+        *reinterpret_cast<uint4*>(dst + (i ? (at0 + 512) ^ 64 : at0)) = decode8(code[g][i][0], sc);
+        *reinterpret_cast<uint4*>(dst + (i ? (at1 + 512) ^ 64 : at1)) = decode8(code[g][i][1], sc);
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
 };
-__device__ __forceinline__ Decoded decode16(const uint4& c, float sc, bool swap) {
-  return {decode8(swap ? c.z : c.x, swap ? c.w : c.y, sc), decode8(swap ? c.x : c.z, swap ? c.y : c.w, sc)};
-}
 
 // The run of this pair or quad: every CTA sums the requests' steps itself.
 // `scratch` is shared memory that nothing else uses yet.

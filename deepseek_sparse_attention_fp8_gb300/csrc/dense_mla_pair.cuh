@@ -22,10 +22,10 @@
 // 131072: 277 us (floors: 46 and 178 by bytes). Of the 85, about 10 pass until
 // the first S (the plan, the table, 208 KB from memory into every pair), 6 go
 // into partials and 5 into joining them.
-// With the fp8 cache the decoding warps bound it (42% of the issue slots of an
-// SM, chains of load, convert and store): 32 requests of 8192 keys 102 us;
-// without its loads 96 of then 113, without its stores 92, without asking rows
-// into L2 ahead 131.
+// With the fp8 cache codes are copied to where half of their values belong and
+// decoded in place: one more stage between a slot's being free and its MMA, and
+// only two steps are in flight. 32 requests of 8192 keys: 103 us, 98 without the
+// arithmetic of decoding, 2 more without asking rows into L2 ahead.
 //
 // Work: the steps of all row tiles form one sequence, cut into equal runs, one
 // per CTA pair (one persistent wave). A row tile cut by a run's end leaves
@@ -138,70 +138,18 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
 
   if (F8 && warp >= kKeyWarp && warp < kKeyWarp + kDecodeWarps) {
     // ---------------- fp8: the own keys of each step, 8 per warp, two groups
-    // (slots) at a time, then the other keys of the step before. A slot's codes
-    // land where its dims 64-127 belong, each key's in its own row: the warp that
-    // has read its keys' codes may write their values in place
-    const int lane8 = lane & 7, key0 = (warp - kKeyWarp) * 8, key = key0 + (lane >> 3);  // and key + 4
-    // the order of a lane's two 16-byte chunks, and of the codes behind them,
-    // that leaves no bank conflicts
-    const uint32_t swap = ((lane8 >> 2) ^ (lane >> 3)) & 1;
-    const uint32_t blk = (lane8 >> 2) * 8192, c0 = 2 * (lane8 & 3);
-    const uint32_t at0 = blk + sw128_offset(key, c0 + swap), at1 = blk + sw128_offset(key, c0 + (swap ^ 1));
-    const uint32_t from = 8192 + key * 128 + 16 * lane8 + 8 * swap;  // and the other 8 codes: ^ 8
-    // two slots; scales: this warp's, of key k and the slot's group in lane
-    // 4 k + sc0 (+ 1); keys from n on do not exist (behind them may lie anything)
-    const auto decode = [&](uint8_t* slot, float scales, int sc0, int n) {
-      uint2 code[2][2][2];  // [slot][key][chunk]
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* at = slot + g * kSlot + 512 * i;
-          code[g][i][0] = *reinterpret_cast<const uint2*>(at + from);
-          code[g][i][1] = *reinterpret_cast<const uint2*>(at + (from ^ 8));
-        }
-      }
-      __syncwarp();
-      if (__any_sync(0xFFFFFFFFu, n < 5)) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (4 * i >= n) code[g][i][0] = code[g][i][1] = make_uint2(0u, 0u);
-        }
-      }
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint8_t* dst = slot + g * kSlot;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float sc = __shfl_sync(0xFFFFFFFFu, scales, 4 * ((lane >> 3) + 4 * i) + sc0 + g);
-          *reinterpret_cast<uint4*>(dst + (i ? (at0 + 512) ^ 64 : at0)) = decode8(code[g][i][0], sc);
-          *reinterpret_cast<uint4*>(dst + (i ? (at1 + 512) ^ 64 : at1)) = decode8(code[g][i][1], sc);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-    };
+    // (slots) at a time, then the other keys of the step before
+    const Decoder d(warp - kKeyWarp, lane);
     Cursor<kPair> c;
     bool more = c.start(p, run), ok = true;
     int kt = c.k0;
     Units u;
     float own_next = 0.f, other_next = 0.f;  // scales of the next step
-    const auto scale_of = [&](Rows x, int group) {
-      float v = 0.f;
-      const int k = key0 + (lane >> 2);
-      if (k < x.n)
-        asm volatile("ld.global.nc.f32 %0, [%1];"
-                     : "=f"(v)
-                     : "l"(p.kv + static_cast<int64_t>(x.row + k) * kF8Row + kDv + 4 * group));
-      return v;
-    };
     const auto fetch_scales = [&] {
       if (kt == c.k0) u.start(p, c, lane, false);
       else u.advance(p, c, kt, lane, false);
-      own_next = scale_of(u.of(p, c, kt, r), lane & 3);
-      other_next = scale_of(u.of(p, c, kt, r ^ 1), 2 * r + (lane & 1));
+      own_next = d.scale(p, u.of(p, c, kt, r), lane & 3, lane);
+      other_next = d.scale(p, u.of(p, c, kt, r ^ 1), 2 * r + (lane & 1), lane);
     };
     if (more) fetch_scales();
     const auto all = [](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
@@ -211,7 +159,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
       const int buf = it & 1, b1 = buf ^ 1;
       const bool last = !more;  // only the other keys of the last step are left
       const float own_scales = own_next, old_scales = other_scales;
-      const int left = c.req.kv_len - kt * kTile - key, old_n = other_n;
+      const int left = c.req.kv_len - kt * kTile - d.key0 - (lane >> 3), old_n = other_n;
       other_scales = other_next;
       other_n = left - 64 * (r ^ 1);
       if (!last) {
@@ -228,12 +176,20 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
       while (h < 2 || other_left) {  // whichever has landed; the other keys are waited for more urgently
         if (other_left && all(mbar_test_wait(&s->other_codes[b1][0], ((it - 1) >> 1) & 1) &&
                               mbar_test_wait(&s->other_codes[b1][1], ((it - 1) >> 1) & 1))) {
-          decode(smem + kSmKv + (b1 * 4 + 2 * (r ^ 1)) * kSlot, old_scales, 0, old_n);
+          uint8_t* slot = smem + kSmKv + (b1 * 4 + 2 * (r ^ 1)) * kSlot;
+          uint2 code[2][2][2];
+          d.read(slot, code[0]);
+          d.read(slot + kSlot, code[1]);
+          d.write(slot, slot + kSlot, code, old_scales, 0, old_n, lane);
           if (lane == 0) mbar_arrive_remote_relaxed(even(&s->other[b1][r ^ 1]));
           other_left = false;
         } else if (h < 2 && all(mbar_test_wait(&s->codes[buf][2 * h], (it >> 1) & 1) &&
                                 mbar_test_wait(&s->codes[buf][2 * h + 1], (it >> 1) & 1))) {
-          decode(smem + kSmKv + (buf * 4 + 2 * h) * kSlot, own_scales, 2 * h, left - 64 * r);
+          uint8_t* slot = smem + kSmKv + (buf * 4 + 2 * h) * kSlot;
+          uint2 code[2][2][2];
+          d.read(slot, code[0]);
+          d.read(slot + kSlot, code[1]);
+          d.write(slot, slot + kSlot, code, own_scales, 2 * h, left - 64 * r, lane);
           if (lane < 2) mbar_arrive_remote_relaxed(even(&s->full[buf][2 * h + lane]));
           ++h;
         } else if (all(clock64() - idle_since > kWaitLimitCycles)) {
@@ -342,8 +298,8 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
       if (it == 0) load_q(row0);  // needs nothing else: ahead of the block table's entries
       Units u;
       u.start(p, c, lane, false);
-      // fp8: the decoding warps' loads are short of registers to run far ahead
-      // in; the own keys of the step kAhead further on are asked into L2
+      // fp8: slots are free too late for copies to hide memory's latency; the own
+      // keys of the step kAhead further on are asked into L2
       Units far = u;
       const auto ask = [&](int kt) {
         const Rows x = far.get(p, c, 2 * kt + r, lane, false);

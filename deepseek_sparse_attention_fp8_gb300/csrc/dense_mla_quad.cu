@@ -19,11 +19,11 @@
 // heads) 2.67 ms, 1.69 PFLOP/s or 0.91 of the measured tensor rate, with 9.0
 // TB/s taken in by the 144 SMs in use: both are nearly full (pairs: 3.58 ms).
 // With the fp8 cache CTAs 0, 1 decode their 64 keys, CTAs 2, 3 their dims of
-// all keys: ~3500 clocks a step. Five chunks of up to 700 tokens over up to
-// 9000 keys: 1.80 ms. The MMAs of S then take 96 clocks instead of 64 each:
-// codes, decoded tiles, P and the MMAs' operands all pass through an SM's
-// shared memory. Without the loads of codes (and with the same decoding) it is
-// 1.43 ms; codes brought by TMA and read from shared memory 1.92.
+// all keys. Codes are copied to where half of their values belong and decoded
+// in place. Five chunks of up to 700 tokens over up to 9000 keys: 1.70 ms (1.45
+// without the arithmetic of decoding). With the codes loaded into registers a
+// step ahead it was 1.80, and 1.43 without those loads: the few KB of L1 beside
+// 227 KB of shared memory hold too few lines in flight.
 #include <algorithm>
 
 #include "dense_mla_pair.cuh"
@@ -238,16 +238,8 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
   } else if (F8 && warp >= kDecodeWarp) {
     // ---------------- fp8: a step's 4 slots of 64 keys x 128 dims (CTAs 0, 1:
     // the 4 groups of the own keys; CTAs 2, 3: the 2 own groups of both units
-    // of keys), 8 keys per warp. A slot's codes land where its dims 64-127
-    // belong, each key's in its own row: the warp that has read its keys' codes
-    // may write their values in place
-    const int lane8 = lane & 7, key0 = (warp - kDecodeWarp) * 8, key = key0 + (lane >> 3);  // and key + 4
-    // the order of a lane's two 16-byte chunks, and of the codes behind them,
-    // that leaves no bank conflicts
-    const uint32_t swap = ((lane8 >> 2) ^ (lane >> 3)) & 1;
-    const uint32_t blk = (lane8 >> 2) * 8192, c0 = 2 * (lane8 & 3);
-    const uint32_t at0 = blk + sw128_offset(key, c0 + swap), at1 = blk + sw128_offset(key, c0 + (swap ^ 1));
-    const uint32_t from = 8192 + key * 128 + 16 * lane8 + 8 * swap;  // and the other 8 codes: ^ 8
+    // of keys), 8 keys per warp
+    const Decoder d(warp - kDecodeWarp, lane);
     const uint32_t full0 = in_cta(&s->full[0], even);
     Ring ring;
     uint32_t phases = 0;  // of the slots' code barriers: q's uses of a slot do not count there
@@ -265,17 +257,12 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
         const Rows x1 = u.of(p, c, kt, 1);
         if (lane & 2) x = x1;
       }
-      const int k = key0 + (lane >> 2), group = values ? 2 * a + (lane & 1) : lane & 3;
-      scale_next = 0.f;
-      if (k < x.n)
-        asm volatile("ld.global.nc.f32 %0, [%1];"
-                     : "=f"(scale_next)
-                     : "l"(p.kv + static_cast<int64_t>(x.row + k) * kF8Row + kDv + 4 * group));
+      scale_next = d.scale(p, x, values ? 2 * a + (lane & 1) : lane & 3, lane);
     };
     if (more) fetch_scales();
     while (more && ok) {
       if (!values && kt == c.k0) ring.next(8);  // q's slots
-      const int left = c.req.kv_len - kt * kTile - key;  // keys that exist: behind them may lie anything
+      const int left = c.req.kv_len - kt * kTile - d.key0 - (lane >> 3);  // keys that exist
       const float scales = scale_next;
       if (++kt == c.k1) {
         more = c.next(p);
@@ -284,43 +271,17 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
       if (more) fetch_scales();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // two slots at a time
-        const int n = left - 64 * (values ? h : a);
         int to[2];
-        uint2 code[2][2][2];  // [slot][key][chunk]
+        uint2 code[2][2][2];
 #pragma unroll
         for (int g = 0; g < 2; ++g, ring.next()) {
           to[g] = ring.slot;
           ok = ok && warp_wait(&s->codes[ring.slot], (phases >> ring.slot) & 1);
           phases ^= 1u << ring.slot;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint8_t* at = smem + to[g] * kSlot + 512 * i;
-            code[g][i][0] = *reinterpret_cast<const uint2*>(at + from);
-            code[g][i][1] = *reinterpret_cast<const uint2*>(at + (from ^ 8));
-          }
+          d.read(smem + to[g] * kSlot, code[g]);
         }
         if (!ok) break;
-        __syncwarp();
-        if (__any_sync(0xFFFFFFFFu, n < 5)) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (4 * i >= n) code[g][i][0] = code[g][i][1] = make_uint2(0u, 0u);
-          }
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint8_t* dst = smem + to[g] * kSlot;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float sc = __shfl_sync(0xFFFFFFFFu, scales, 4 * ((lane >> 3) + 4 * i) + 2 * h + g);
-            *reinterpret_cast<uint4*>(dst + (i ? (at0 + 512) ^ 64 : at0)) = decode8(code[g][i][0], sc);
-            *reinterpret_cast<uint4*>(dst + (i ? (at1 + 512) ^ 64 : at1)) = decode8(code[g][i][1], sc);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
+        d.write(smem + to[0] * kSlot, smem + to[1] * kSlot, code, scales, 2 * h, left - 64 * (values ? h : a), lane);
         if (lane < 2) mbar_arrive_remote_relaxed(full0 + 8 * (lane ? to[1] : to[0]));
       }
     }

@@ -14,6 +14,12 @@
 // Of the rest ~9 us are the way to the first S (the plan, the table, the first
 // 144 KB), ~2 us results, ~5 us the joining of partials.
 //
+// fp8 cache (16 rows): codes are copied to where half of their values belong
+// and decoded in place, a slot of 128 keys x 128 dims at a time. 64 requests of
+// 4096 keys, 16 heads (172 MB, 25 us): 87 us, 110 on pairs; 82 without the
+// arithmetic of decoding. Decoding from loads into registers a step ahead took
+// 108, 77 without those loads.
+//
 // Rope dims come first in a step: their slots are free again after S, so that a
 // third of the next step is loaded while this one's weights are made. Results
 // are written by code that fits few cache lines of instructions, and a row's
