@@ -349,7 +349,7 @@ struct Decoder {
   }
 };
 
-// The run of this pair or quad: every CTA sums the requests' steps itself.
+// The run of this pair, quad or single CTA: every CTA sums the requests' steps.
 // `scratch` is shared memory that nothing else uses yet.
 //
 // kQuad: in clusters of four CTAs the lengths, which only the device knows,
