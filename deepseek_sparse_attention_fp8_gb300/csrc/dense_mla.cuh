@@ -13,6 +13,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "dense_steps.h"
 #include "ptx.cuh"
 
 namespace dsa {
@@ -23,7 +24,6 @@ using namespace ptx;
 constexpr int kDk = 576, kDv = 512, kF8Row = 656;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kTile = 128;    // keys of a step
 constexpr int kSlot = 16384;  // 64 keys x 128 dims
 constexpr float kRescaleThreshold = 8.f;  // log2 units
 constexpr long long kWaitLimitCycles = 2000000000ll;
@@ -75,67 +75,10 @@ __device__ __forceinline__ bool misaligned(const DenseParams& p, const uint8_t* 
   return true;
 }
 
-// A request's rows as work: row tile i has steps(i) = max(1, ceil(keys its
-// last token sees / 128)).
-struct Request {
-  int32_t q0, q_len, n_tiles, kv_len;  // kv_len: its cached keys that the table can hold
-  int32_t c;     // position of its first new token (a length below 0 counts as 0)
-  bool uneven;   // lengths that contradict each other: every tile is charged kv_len
-};
-
+// The request b of the batch, as work.
 __device__ __forceinline__ Request load_request(const DenseParams& p, int tpt, int b) {
-  Request r;
-  const int q0 = min(max(__ldg(p.qsl + b), 0), p.T), q1 = min(max(__ldg(p.qsl + b + 1), 0), p.T);
-  const int64_t sl = __ldg(p.seq_lens + b), cap = static_cast<int64_t>(p.bt_stride) * p.block_size;
-  r.q0 = q0;
-  r.q_len = max(q1 - q0, 0);
-  r.n_tiles = (r.q_len + tpt - 1) / tpt;
-  // at most 2^31 - 256, so that sums of a few steps stay within 31 bits
-  r.kv_len = static_cast<int32_t>(max(int64_t(0), min(min(sl, cap), int64_t(0x7FFFFF00))));
-  r.c = static_cast<int32_t>(max(sl, int64_t(0))) - r.q_len;
-  r.uneven = r.c < 0 || r.kv_len != sl;
-  return r;
-}
-// keys visible to the token i (from 0) of the request
-__device__ __forceinline__ int visible(const Request& r, int i) {
-  return max(0, min(r.c + i + 1, r.kv_len));
-}
-__device__ __forceinline__ int steps_of(const Request& r, int tpt, int tile) {
-  const int keys = r.uneven ? r.kv_len : visible(r, min(r.q_len, (tile + 1) * tpt) - 1);
-  return max(1, (keys + kTile - 1) / kTile);
-}
-// sum over i < n of floor((a i + b) / 128)
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
-  if ((a & (a - 1)) == 0) {  // a divides 128: floor((i + b / a) / (128 / a)), a whole run of each quotient
-    const int sh = 7 - (31 - __clz(static_cast<int>(a)));
-    const auto upto = [&](int64_t x) {  // sum over j < x of floor(j / 2^sh)
-      const int64_t k = x >> sh;
-      return ((k * (k - 1) / 2) << sh) + k * (x & ((int64_t(1) << sh) - 1));
-    };
-    const int64_t b0 = b / a;
-    return upto(n + b0) - upto(b0);
-  }
-  // the lattice points under the line, by the Euclidean algorithm
-  int64_t sum = 0, m = 128;
-  while (true) {
-    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const int64_t top = a * n + b;
-    if (top < m) return sum;
-    n = top / m;
-    b = top % m;
-    const int64_t t = m;
-    m = a;
-    a = t;
-  }
-}
-// steps of the request's first n row tiles (of n_tiles) of tpt tokens
-__device__ __forceinline__ int64_t steps_before(const Request& r, int tpt, int n_tiles, int n) {
-  if (r.uneven) return static_cast<int64_t>(n) * steps_of(r, tpt, 0);
-  if (n == 0) return 0;
-  const int64_t b = static_cast<int64_t>(r.c) + tpt + kTile - 1;
-  return n < n_tiles ? floor_sum(n, tpt, b) : floor_sum(n - 1, tpt, b) + steps_of(r, tpt, n - 1);
+  return make_request(min(max(__ldg(p.qsl + b), 0), p.T), min(max(__ldg(p.qsl + b + 1), 0), p.T), __ldg(p.seq_lens + b),
+                      static_cast<int64_t>(p.bt_stride) * p.block_size, tpt);
 }
 
 // A run of steps, segment by segment (a segment: the steps of one row tile).
