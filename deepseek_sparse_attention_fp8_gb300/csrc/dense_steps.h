@@ -45,7 +45,8 @@ DSA_STEPS_FN int visible(const Request& r, int i) {
 DSA_STEPS_FN int steps_of(const Request& r, int tpt, int tile) {
   const int end = (tile + 1) * tpt < r.q_len ? (tile + 1) * tpt : r.q_len;
   const int keys = r.uneven ? r.kv_len : visible(r, end - 1);
-  return keys > kTile ? (keys + kTile - 1) / kTile : 1;
+  const int steps = (keys + kTile - 1) / kTile;
+  return steps > 1 ? steps : 1;
 }
 // sum over i < n of floor((a i + b) / 128)
 DSA_STEPS_FN int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
