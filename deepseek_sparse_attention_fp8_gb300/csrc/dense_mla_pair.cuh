@@ -181,6 +181,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
           d.read(slot, code[0]);
           d.read(slot + kSlot, code[1]);
           d.write(slot, slot + kSlot, code, old_scales, 0, old_n, lane);
+          fence_release_smem();
           if (lane == 0) mbar_arrive_remote_relaxed(even(&s->other[b1][r ^ 1]));
           other_left = false;
         } else if (h < 2 && all(mbar_test_wait(&s->codes[buf][2 * h], (it >> 1) & 1) &&
@@ -190,6 +191,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
           d.read(slot, code[0]);
           d.read(slot + kSlot, code[1]);
           d.write(slot, slot + kSlot, code, own_scales, 2 * h, left - 64 * r, lane);
+          fence_release_smem();
           if (lane < 2) mbar_arrive_remote_relaxed(even(&s->full[buf][2 * h + lane]));
           ++h;
         } else if (all(clock64() - idle_since > kWaitLimitCycles)) {
@@ -344,8 +346,9 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
       long long idle_since = clock64();
       while ((more || ip < iq) && !__any_sync(0xFFFFFFFFu, s->abort)) {
         bool progressed = false;
-        if (ip < iq && all(half == 0 ? mbar_test_wait(&s->p_full, ip & 1) && mbar_test_wait(&s->other[ip & 1][0], (ip >> 1) & 1)
-                                     : mbar_test_wait(&s->other[ip & 1][1], (ip >> 1) & 1))) {
+        if (ip < iq && all((half == 1 || mbar_test_wait_relaxed(&s->p_full, ip & 1)) &&
+                           mbar_test_wait_relaxed(&s->other[ip & 1][half], (ip >> 1) & 1))) {
+          fence_acquire_smem();
           tc_fence_after();
           const int buf = ip & 1;
           const uint32_t a0 = k_lo + ((kSmP + half * 8192) >> 4);
@@ -368,9 +371,11 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
         }
         if (more && iq < ip + 2) {  // PV of step iq - 2 has been issued: S was read
           const int buf = iq & 1;
-          bool ready = sub < 4 ? mbar_test_wait(&s->full[buf][sub], (iq >> 1) & 1) : mbar_test_wait(&s->rope, iq & 1);
-          if (sub == 0 && kt == c.k0) ready = ready && mbar_test_wait(&s->q, segs & 1);
+          bool ready = sub < 4 ? mbar_test_wait_relaxed(&s->full[buf][sub], (iq >> 1) & 1)
+                               : mbar_test_wait_relaxed(&s->rope, iq & 1);
+          if (sub == 0 && kt == c.k0) ready = ready && mbar_test_wait_relaxed(&s->q, segs & 1);
           if (all(ready)) {
+            fence_acquire_smem();
             tc_fence_after();
             const uint32_t d = tmem + kColS + 64 * buf;
             if (sub < 4) {
@@ -417,10 +422,10 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
     // group take 32 keys (and 128 columns of O) each
     const int l128 = (warp & 3) * 32 + lane, row = l128 & 63, kh = l128 >> 6, half = warp >> 2;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    // P stays in this CTA's shared memory, whose tensor core reads it there:
-    // the proxy fence before the arrival orders the data, and only the arrival
-    // itself crosses to the even CTA. (A release at cluster scope instead took
-    // 1300-2000 clocks per step.)
+    // P stays in this CTA's shared memory, whose tensor core reads it there: the
+    // proxy fence makes it visible to that core, the release of shared memory to
+    // the even CTA, which issues the MMA. (A release at cluster scope of all
+    // memory instead took 1300-2000 clocks per step.)
     const uint32_t p_full = even(&s->p_full);
     uint8_t* p_dst = smem + kSmP + kh * 8192;
     Cursor<kPair> c;
@@ -513,6 +518,7 @@ __device__ __forceinline__ void run_pair(const DenseParams& p, const Maps& maps,
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
+        fence_release_smem();
         if (lane == 0) mbar_arrive_remote_relaxed(p_full);
       }
       if (!ok) break;

@@ -96,6 +96,20 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
+// The probe of a phase that arrivals from other CTAs complete, without memory
+// ordering: fence_acquire_smem follows a success.
+__device__ __forceinline__ bool mbar_test_wait_relaxed(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
@@ -116,6 +130,18 @@ __device__ __forceinline__ void cluster_sync_all() {
 // loads have completed, place it after instructions that consume their values.
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// Release and acquire at cluster scope for objects in shared memory alone. A
+// fence_release_smem, then a relaxed arrival on a barrier of another CTA; there
+// a test at cluster scope that succeeds, then fence_acquire_smem: what the one
+// thread has written to its CTA's shared memory, or seen its CTA's threads
+// release, comes before what the other does next. (fence.acq_rel.cluster waits
+// for global memory too: 750-1400 clocks while copies stream in.)
+__device__ __forceinline__ void fence_release_smem() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void fence_acquire_smem() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 // Asynchronous 16-byte store into a peer CTA's shared memory; completion is
 // counted (as transaction bytes) on the peer's mbarrier at `cluster_bar`.
