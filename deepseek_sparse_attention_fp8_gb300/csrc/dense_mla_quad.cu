@@ -34,8 +34,8 @@ namespace {
 
 // Warps 0-7: softmax (CTAs 0, 1), rescaling and results (CTAs 2, 3); 8 TMA
 // loads, 9 MMA, 10 P on its way (CTAs 0, 1); with the fp8 cache 12-19 decode
-// keys and values (11 is idle).
-constexpr int kWorkers = 8, kLoadWarp = 8, kMmaWarp = 9, kSendWarp = 10, kDecodeWarp = 12, kDecodeWarps = 8;
+// keys and values, 11 tells the even CTA of the odd one's.
+constexpr int kWorkers = 8, kLoadWarp = 8, kMmaWarp = 9, kSendWarp = 10, kHandWarp = 11, kDecodeWarp = 12, kDecodeWarps = 8;
 template <bool F8>
 constexpr int kThreadsOf = F8 ? 640 : 352;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColQ = 256;  // CTAs 0, 1: S 2 x 128, q 256; CTAs 2, 3: O 512
@@ -97,6 +97,13 @@ __device__ __forceinline__ void st_async_v2(uint32_t cluster_addr, uint32_t clus
                "r"(a), "r"(b), "r"(cluster_bar)
                : "memory");
 }
+// for phases that other CTAs' arrivals complete, behind a release of their
+// shared memory (of tensor memory alone: behind tc_fence_before)
+__device__ __forceinline__ bool warp_wait_acquire_smem(uint64_t* bar, uint32_t parity) {
+  const bool ok = mbar_wait_relaxed(bar, parity);
+  fence_acquire_smem();
+  return __all_sync(0xFFFFFFFFu, ok);
+}
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity));
 }
@@ -128,7 +135,7 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
 
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&s->full[i], F8 ? 2 * kDecodeWarps : 1);
+      mbar_init(&s->full[i], F8 ? kDecodeWarps + (a == 0 ? 1 : 0) : 1);  // even CTAs: and the odd one's, handed on
       mbar_init(&s->empty[i], 1);
       mbar_init(&s->codes[i], 1);
     }
@@ -240,7 +247,6 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
     // the 4 groups of the own keys; CTAs 2, 3: the 2 own groups of both units
     // of keys), 8 keys per warp
     const Decoder d(warp - kDecodeWarp, lane);
-    const uint32_t full0 = in_cta(&s->full[0], even);
     Ring ring;
     uint32_t phases = 0;  // of the slots' code barriers: q's uses of a slot do not count there
     Units u;
@@ -282,10 +288,37 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
         }
         if (!ok) break;
         d.write(smem + to[0] * kSlot, smem + to[1] * kSlot, code, scales, 2 * h, left - 64 * (values ? h : a), lane);
-        if (lane < 2) mbar_arrive_remote_relaxed(full0 + 8 * (lane ? to[1] : to[0]));
+        if (lane < 2) mbar_arrive(&s->full[lane ? to[1] : to[0]]);
       }
     }
     if (!ok && lane == 0) abort_now();
+  } else if (F8 && warp == kHandWarp) {
+    // ---------------- fp8: the odd CTA's decoded slots to the even one, whose warp
+    // issues the MMAs, two at a time. A fence in the decoding warps themselves
+    // would wait for the scales that they have in flight
+    if (a == 1) {
+      const uint32_t full0 = in_cta(&s->full[0], even);
+      Ring ring;
+      uint32_t phases = 0;
+      bool ok = true;
+      for (bool more = c.start(p, run); more && ok; more = c.next(p)) {
+        if (!values) ring.next(8);
+        for (int i = 2 * (c.k1 - c.k0); i > 0 && ok; --i) {
+          int of[2];
+#pragma unroll
+          for (int g = 0; g < 2; ++g, ring.next()) {
+            of[g] = ring.slot;
+            ok = ok && warp_wait(&s->full[ring.slot], (phases >> ring.slot) & 1);
+            phases ^= 1u << ring.slot;
+          }
+          if (!ok) break;
+          fence_release_smem();
+          if (lane < 2) mbar_arrive_remote_relaxed(full0 + 8 * (lane ? of[1] : of[0]));
+        }
+      }
+      if (!ok && lane == 0) abort_now();
+    }
+    __syncwarp();
   } else if (warp == kLoadWarp) {
     // ---------------- all keys of each step, the own value dims
     Ring ring;
@@ -325,14 +358,14 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
       int it = 0, seg = 0;
       for (bool more = c.start(p, run); more && ok; more = c.next(p), ++seg) {
         ring.next(8);
-        ok = warp_wait(&s->q_ready, seg & 1);
+        ok = warp_wait_acquire_smem(&s->q_ready, seg & 1);
         for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
           const int buf = it & 1;
-          if (it >= 2) ok = warp_wait(&s->s_free[buf], ((it >> 1) - 1) & 1);
+          if (it >= 2) ok = warp_wait_acquire_smem(&s->s_free[buf], ((it >> 1) - 1) & 1);
           const uint32_t d = tmem + kColS + 128 * buf;
 #pragma unroll 1
           for (int k = 0; k < 4 && ok; ++k, ring.next()) {
-            ok = warp_wait(&s->full[ring.slot], (phases >> ring.slot) & 1);
+            ok = warp_wait_acquire_smem(&s->full[ring.slot], (phases >> ring.slot) & 1);
             if (!ok) break;
             phases ^= 1u << ring.slot;
             tc_fence_after();
@@ -346,7 +379,7 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
             }
             __syncwarp();
           }
-          ok = ok && warp_wait(&s->rope_full[buf], (it >> 1) & 1);
+          ok = ok && warp_wait_acquire_smem(&s->rope_full[buf], (it >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint32_t b0 = k_lo + ((kSmRopeK + buf * 8192) >> 4);
@@ -379,14 +412,14 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
       for (bool more = c.start(p, run); more && ok; more = c.next(p)) {
         for (int kt = c.k0; kt < c.k1 && ok; ++kt, ++it) {
           const int buf = it & 1;
-          ok = warp_wait(&s->p_ready[buf], (it >> 1) & 1);
+          ok = warp_wait_acquire_smem(&s->p_ready[buf], (it >> 1) & 1);
 #pragma unroll 1
           for (int kh = 0; kh < 2 && ok; ++kh) {  // 64 keys each: a slot of 128 dims after the other
             const int s0 = ring.slot;
-            ok = warp_wait(&s->full[ring.slot], ring.turn & 1);
+            ok = warp_wait_acquire_smem(&s->full[ring.slot], ring.turn & 1);
             ring.next();
             const int s1 = ring.slot;
-            ok = ok && warp_wait(&s->full[ring.slot], ring.turn & 1);
+            ok = ok && warp_wait_acquire_smem(&s->full[ring.slot], ring.turn & 1);
             ring.next();
             if (!ok) break;
             tc_fence_after();
@@ -631,6 +664,7 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
         }
         tc_fence_before();
         __syncwarp();
+        fence_release_smem();  // P and the factors have landed, O is rescaled
         if (lane == 0) mbar_arrive_remote_relaxed(p_ready + 8 * buf);
       }
       if (!ok) break;

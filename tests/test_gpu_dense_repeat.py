@@ -3,7 +3,7 @@ the last bit, so that an access that two CTAs do not order would be seen."""
 import pytest
 import torch
 
-from dense_kinds import PAIR, kinds
+from dense_kinds import PAIR, QUAD, kinds, takes_quads
 from dense_testlib import DV, SCALE, check_dense, dense_reference, make_dense_case
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +35,10 @@ def repeat(c, kind, calls):
 @pytest.mark.parametrize("lens,q_lens,H", [([8192] * 16, [1] * 16, 128), ([900, 300, 2000, 64] * 8, [1] * 32, 100)])
 def test_pairs(lens, q_lens, H, fp8):
     repeat(make_dense_case(lens, q_lens, H, fp8=fp8, seed=61), PAIR, 600)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,q_lens,H", [([9000, 5000, 12000], [16, 40, 8], 128), ([6100, 3000], [150, 90], 40)])
+def test_quads(lens, q_lens, H, fp8):
+    assert takes_quads(lens, q_lens, H)
+    repeat(make_dense_case(lens, q_lens, H, fp8=fp8, seed=62), QUAD, 600)
