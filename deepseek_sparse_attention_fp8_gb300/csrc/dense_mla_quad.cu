@@ -618,7 +618,7 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
       ok = meet();
       l = sums[row] + sums[128 + row];
       ok = ok && meet();
-      if (ok && seg > 0 && half == 0) ok = warp_wait(&s->ml_free, (seg - 1) & 1);
+      if (ok && seg > 0 && half == 0) ok = warp_wait_acquire_smem(&s->ml_free, (seg - 1) & 1);
       if (!ok) {
         if (lane == 0) abort_now();
         break;
@@ -642,8 +642,8 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
         if (tid == 0) mbar_arrive_expect_tx(&s->p_full[buf], 32768 + 512);
         __syncwarp();
         ok = warp_wait_cluster(&s->p_full[buf], (it >> 1) & 1);
-        const float alpha = ok ? alphas[buf * 128 + row] : 1.f;
-        if (ok && kt > c.k0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+        const float alpha = ok && kt > c.k0 ? alphas[buf * 128 + row] : 1.f;  // (a row tile begins with any)
+        if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {
           ok = warp_wait(&s->pv_done[buf ^ 1], ((it - 1) >> 1) & 1);
           if (ok) {
             tc_fence_after();
@@ -677,9 +677,9 @@ __device__ __forceinline__ void run_quad(const DenseParams& p, const Maps& maps,
         if (lane == 0) abort_now();
         break;
       }
-      // the value is consumed before the arrival lets it be overwritten
-      asm volatile("" ::"f"(ml.x), "f"(ml.y) : "memory");
+      // the reads come before the arrival that lets CTA a write the next row tile's
       __syncwarp();
+      fence_release_smem();
       if (lane == 0) mbar_arrive_remote_relaxed(ml_free);
       tc_fence_after();
       const int in_tile = 128 * a + row;

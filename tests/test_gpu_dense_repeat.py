@@ -42,3 +42,11 @@ def test_pairs(lens, q_lens, H, fp8):
 def test_quads(lens, q_lens, H, fp8):
     assert takes_quads(lens, q_lens, H)
     repeat(make_dense_case(lens, q_lens, H, fp8=fp8, seed=62), QUAD, 600)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_quads_of_several_row_tiles(fp8):
+    """A run of many row tiles: maxima and sums go to the output CTAs tile after tile."""
+    lens, q_lens = [900, 700, 800], [200, 151, 177]
+    assert takes_quads(lens, q_lens, 128)
+    repeat(make_dense_case(lens, q_lens, 128, fp8=fp8, seed=63), QUAD, 300)
