@@ -248,11 +248,11 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = tmem_holder;
 
-  // Launched as a programmatic dependent of the top-k. q, query_start_loc and
-  // seq_lens are inputs of the step that no kernel of the library writes, so
-  // this CTA's q K-blocks (by TMA, into KV stages kQStage..., which tiles 0
-  // and 1 leave untouched) and the token's request are fetched before the
-  // wait, overlapping the top-k's tail; the top-k slots are read after it.
+  // Launched as a programmatic dependent of the top-k. q is an input of the step
+  // that no kernel of the library writes, so this CTA's q K-blocks are fetched
+  // before the wait (by TMA, into KV stages kQStage..., which tiles 0 and 1
+  // leave untouched), overlapping the top-k's tail; the top-k slots and the
+  // lengths are read after it.
   uint8_t* q_stage = kv_sm + L::kQStage * L::kKvStage;
   if (tid == kProdWarp0 * 32) {  // first producer thread
     prefetch_tmap(&qmap);
@@ -267,6 +267,19 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_kernel(const __grid_co
       tma_load_3d(smem_u32(q_stage + kb * 16384), &qmap, &q_full, (kb0 + kb) * 64, 0, t);
     if constexpr (C::kRopeHalf) tma_load_3d(smem_u32(q_stage + nkb * 16384), &qmap64, &q_full, rope_x, 0, t);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the top-k's results are visible from here on
+  const int slot0 = j * p.per_split;
+  const int n_slots = max(0, min(p.K, slot0 + p.per_split) - slot0);
+  const int32_t* idx_row = p.topk + static_cast<int64_t>(t) * p.K + slot0;
+  int idx[8];
+  if (warp < 8) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int sl = u * 256 + tid;
+      idx[u] = sl < n_slots ? __ldg(idx_row + sl) : -1;
+    }
+  }
+
   // the request of token t: the last b with query_start_loc[b] <= t, found in
   // one round of loads when the batch has at most kThreads requests
   int b, q0, q1, sl_b;
@@ -292,19 +305,6 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_mla_kernel(const __grid_co
     valid64 = max(static_cast<int64_t>(0), min(valid64, cap));
   }
   const int valid = static_cast<int>(valid64);
-
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the top-k's results are visible from here on
-  const int slot0 = j * p.per_split;
-  const int n_slots = max(0, min(p.K, slot0 + p.per_split) - slot0);
-  const int32_t* idx_row = p.topk + static_cast<int64_t>(t) * p.K + slot0;
-  int idx[8];
-  if (warp < 8) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int sl = u * 256 + tid;
-      idx[u] = sl < n_slots ? __ldg(idx_row + sl) : -1;
-    }
-  }
 
   auto abort_now = [&](void) {
     s_abort = 1;

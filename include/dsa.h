@@ -38,11 +38,10 @@
  *     runs out sets DSA_DEVERR_TIMEOUT and the kernel returns.
  *   - The top-k, attention and merge kernels are launched as programmatic
  *     dependents of the kernel before them on the stream. Before waiting for
- *     it they read only inputs that no kernel of this library writes (q) or
- *     that only dsa_build_batch writes, which never lets its dependents start
- *     early (seq_lens, query_start_loc); a caller's kernel placed directly
- *     before them that lets its dependents start early must not write those.
- *     The dense attention kernels read nothing before waiting.
+ *     it the sparse attention kernels read q, which no kernel of this library
+ *     writes: a caller's kernel placed directly before them that lets its
+ *     dependents start early must not write it. The others read nothing before
+ *     waiting.
  *   - Request b owns query tokens [query_start_loc[b], query_start_loc[b+1]);
  *     q_len_b is their count. seq_lens[b] counts the request's cached keys
  *     INCLUDING its q_len_b new tokens, so query token t of request b sits at
