@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kThreads) k_quant_cache_kernel(const uint16_t*
 
   // request of token t: the last b with query_start_loc[b] <= t, counted by
   // the warp's lanes over strided entries (independent loads, one round)
+  const int end = __ldg(qsl + B);
   int cnt = 0;
 #pragma unroll 4
   for (int j = lane; j < B; j += 32) cnt += __ldg(qsl + j) <= t ? 1 : 0;
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(kThreads) k_quant_cache_kernel(const uint16_t*
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
   const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
 
+  if (t >= end) return;  // a padded batch's token: of no request
   if (pos < 0 || pos >= static_cast<int64_t>(bt_stride) * block_size) {
     if (lane == 0) report(dev_status, DSA_DEVERR_SEQ_LEN);
     return;
@@ -135,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) mla_kv_fp8_cache_kernel(const uint16
   }
 
   // request and position of token t (as for the indexer keys above)
+  const int end = __ldg(qsl + B);
   int cnt = 0;
 #pragma unroll 4
   for (int j = lane; j < B; j += 32) cnt += __ldg(qsl + j) <= t ? 1 : 0;
@@ -152,6 +155,7 @@ __global__ void __launch_bounds__(kThreads) mla_kv_fp8_cache_kernel(const uint16
   for (int off = 1; off < 8; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
   const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
 
+  if (t >= end) return;  // a padded batch's token: of no request
   if (pos < 0 || pos >= static_cast<int64_t>(bt_stride) * block_size) {
     if (lane == 0) report(dev_status, DSA_DEVERR_SEQ_LEN);
     return;

@@ -153,9 +153,10 @@ dsa_status_t dsa_indexer_logits(const void* q_idx, int64_t q_stride_t, const flo
  * e4m3_rn_satfinite(k / scale), both divisions IEEE-rounded fp32: the rule of
  * a0 applied to the key row (finite inputs). A position outside the block
  * table (DSA_DEVERR_SEQ_LEN) or a block id outside [0, num_blocks)
- * (DSA_DEVERR_BLOCK_OOB) skips that token. Supported: Di in {32, 64, 128};
- * block_size a multiple of 64. Tokens must not share a position (each writes
- * its row without ordering against the others).
+ * (DSA_DEVERR_BLOCK_OOB) skips that token; tokens from query_start_loc[B] on
+ * (a padded batch) are skipped too, without a status bit. Supported: Di in
+ * {32, 64, 128}; block_size a multiple of 64. Tokens must not share a position
+ * (each writes its row without ordering against the others).
  */
 dsa_status_t dsa_indexer_k_quant_and_cache(const void* k, int64_t k_stride_t, int32_t T, int32_t Di, uint8_t* k_cache,
                                            int64_t k_block_stride_bytes, int32_t num_blocks,
@@ -309,8 +310,9 @@ dsa_status_t sparse_mla_prefill_fp8(const void* q, const uint8_t* kv_cache, int6
  * amax/448 (1 when amax == 0) and code = e4m3_rn_satfinite(x / scale), both
  * divisions IEEE-rounded fp32; the 64 rope dims keep their bf16 bits. A
  * position outside the block table (DSA_DEVERR_SEQ_LEN) or a block id outside
- * [0, num_blocks) (DSA_DEVERR_BLOCK_OOB) skips that token. Supported: (Dk, Dv)
- * = (576, 512), block_size a multiple of 64.
+ * [0, num_blocks) (DSA_DEVERR_BLOCK_OOB) skips that token; tokens from
+ * query_start_loc[B] on (a padded batch) are skipped too, without a status bit.
+ * Supported: (Dk, Dv) = (576, 512), block_size a multiple of 64.
  */
 dsa_status_t dsa_mla_kv_fp8_quant_and_cache(const void* kv, int64_t kv_stride_t, int32_t T, int32_t Dk, int32_t Dv,
                                             uint8_t* kv_cache, int64_t kv_block_stride_bytes, int32_t num_blocks,
