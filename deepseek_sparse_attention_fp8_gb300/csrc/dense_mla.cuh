@@ -77,8 +77,9 @@ __device__ __forceinline__ bool misaligned(const DenseParams& p, const uint8_t* 
 
 // The request b of the batch, as work.
 __device__ __forceinline__ Request load_request(const DenseParams& p, int tpt, int b) {
-  return make_request(min(max(__ldg(p.qsl + b), 0), p.T), min(max(__ldg(p.qsl + b + 1), 0), p.T), __ldg(p.seq_lens + b),
-                      static_cast<int64_t>(p.bt_stride) * p.block_size, tpt);
+  const int q0 = min(max(__ldg(p.qsl + b), 0), p.T), q1 = min(max(__ldg(p.qsl + b + 1), 0), p.T);
+  const int64_t sl = __ldg(p.seq_lens + b), cap = static_cast<int64_t>(p.bt_stride) * p.block_size;
+  return make_request(q0, q1, sl, cap, tpt);
 }
 
 // A run of steps, segment by segment (a segment: the steps of one row tile).

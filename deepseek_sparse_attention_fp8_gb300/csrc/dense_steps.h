@@ -1,6 +1,7 @@
 // A dense attention batch as row tiles and steps of 128 keys: whole numbers
 // only, for the kernels and, compiled by a host compiler, for the tests.
 #pragma once
+#include <algorithm>
 #include <cstdint>
 
 #ifdef __CUDACC__
@@ -11,6 +12,11 @@
 
 namespace dsa {
 namespace dense {
+
+#ifndef __CUDACC__
+using std::max;
+using std::min;
+#endif
 
 constexpr int kTile = 128;  // keys of a step
 
@@ -27,26 +33,21 @@ struct Request {
 DSA_STEPS_FN Request make_request(int32_t q0, int32_t q1, int64_t sl, int64_t cap, int tpt) {
   Request r;
   r.q0 = q0;
-  r.q_len = q1 > q0 ? q1 - q0 : 0;
+  r.q_len = max(q1 - q0, 0);
   r.n_tiles = (r.q_len + tpt - 1) / tpt;
   // at most 2^31 - 256, so that sums of a few steps stay within 31 bits
-  int64_t kv = sl < cap ? sl : cap;
-  kv = kv < 0x7FFFFF00 ? kv : 0x7FFFFF00;
-  r.kv_len = static_cast<int32_t>(kv > 0 ? kv : 0);
-  r.c = static_cast<int32_t>(sl > 0 ? sl : 0) - r.q_len;
+  r.kv_len = static_cast<int32_t>(max(int64_t(0), min(min(sl, cap), int64_t(0x7FFFFF00))));
+  r.c = static_cast<int32_t>(max(sl, int64_t(0))) - r.q_len;
   r.uneven = r.c < 0 || r.kv_len != sl;
   return r;
 }
 // keys visible to the token i (from 0) of the request
 DSA_STEPS_FN int visible(const Request& r, int i) {
-  const int n = r.c + i + 1 < r.kv_len ? r.c + i + 1 : r.kv_len;
-  return n > 0 ? n : 0;
+  return max(0, min(r.c + i + 1, r.kv_len));
 }
 DSA_STEPS_FN int steps_of(const Request& r, int tpt, int tile) {
-  const int end = (tile + 1) * tpt < r.q_len ? (tile + 1) * tpt : r.q_len;
-  const int keys = r.uneven ? r.kv_len : visible(r, end - 1);
-  const int steps = (keys + kTile - 1) / kTile;
-  return steps > 1 ? steps : 1;
+  const int keys = r.uneven ? r.kv_len : visible(r, min(r.q_len, (tile + 1) * tpt) - 1);
+  return max(1, (keys + kTile - 1) / kTile);
 }
 // sum over i < n of floor((a i + b) / 128)
 DSA_STEPS_FN int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
