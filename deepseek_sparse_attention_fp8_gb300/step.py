@@ -11,7 +11,8 @@ attention queries q into a second, `inputs_q`; the outputs (out, lse) into a
 third, `outputs`; each tensor at a 256-byte aligned offset. A caller that
 stages a step's inputs in host memory moves them with one copy per buffer
 (`run_host` overlaps the queries' copy with the indexer and top-k). The
-caches stay resident in their own buffers.
+caches stay resident in their own buffers. A dense step has no indexer and no
+top-k: it holds and moves nothing that only they read or write.
 """
 from __future__ import annotations
 
@@ -83,16 +84,17 @@ class DsaStep:
         # per-step inputs in two buffers: what the indexer and top-k read, and
         # the attention queries (copied from the host in parallel with those
         # kernels by run_host)
-        ins = [(wl.q_idx, torch.bfloat16), (wl.w, torch.float32), (wl.block_table, torch.int32),
-               (wl.seq_lens, torch.int32), (wl.query_start_loc, torch.int32)]
+        ins = [] if dense else [(wl.q_idx, torch.bfloat16), (wl.w, torch.float32)]
+        ins += [(wl.block_table, torch.int32), (wl.seq_lens, torch.int32), (wl.query_start_loc, torch.int32)]
         self.inputs, views = _packed([(np.shape(a), dt) for a, dt in ins], d)
         for v, (a, dt) in zip(views, ins):
             v.copy_(_host(a, dt))
-        self.q_idx, self.w, self.block_table, self.seq_lens, self.qsl = views
+        self.q_idx, self.w = (None, None) if dense else views[:2]
+        self.block_table, self.seq_lens, self.qsl = views[-3:]
         self.inputs_q, (self.q,) = _packed([(np.shape(wl.q), torch.bfloat16)], d)
         self.q.copy_(_host(wl.q, torch.bfloat16))
         self._side = None
-        self.k_cache = _dev(wl.k_cache, torch.uint8, d)
+        self.k_cache = None if dense else _dev(wl.k_cache, torch.uint8, d)
         # the latent cache: bf16 rows, or (kv_fp8) the workload's fp8 rows
         self.kv_fp8 = kv_fp8
         if kv_fp8:
@@ -101,8 +103,12 @@ class DsaStep:
             self.kv_cache = _dev(wl.kv_cache_fp8, torch.uint8, d)
         else:
             self.kv_cache = _dev(wl.kv_cache, torch.bfloat16, d)
-        self.logits = torch.empty((wl.T, wl.ld), dtype=torch.float32, device=d)
-        self.topk_idx = torch.empty((wl.T, wl.index_topk), dtype=torch.int32, device=d)
+        self.logits = self.topk_idx = self.ws_topk = None
+        if not dense:
+            self.logits = torch.empty((wl.T, wl.ld), dtype=torch.float32, device=d)
+            self.topk_idx = torch.empty((wl.T, wl.index_topk), dtype=torch.int32, device=d)
+            ws_topk = api.dsa_topk_workspace_size(wl.T, wl.ld, wl.index_topk)
+            self.ws_topk = torch.empty(max(ws_topk, 16), dtype=torch.uint8, device=d)
         self.outputs, (self.out, self.lse) = _packed([((wl.T, wl.H, wl.Dv), torch.bfloat16),
                                                       ((wl.T, wl.H), torch.float32)], d)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=d)
@@ -115,18 +121,22 @@ class DsaStep:
             self.splits = 1 if self.prefill else api.sparse_mla_num_splits(wl.T, wl.H, wl.Dv, wl.index_topk,
                                                                              num_kv_splits)
             ws_mla = api.sparse_mla_workspace_size(wl.T, wl.H, wl.Dv, self.splits)
-        ws_topk = api.dsa_topk_workspace_size(wl.T, wl.ld, wl.index_topk)
-        self.ws_topk = torch.empty(max(ws_topk, 16), dtype=torch.uint8, device=d)
         self.ws_mla = torch.empty(max(ws_mla, 16), dtype=torch.uint8, device=d)
 
     def _range(self, name):
         return torch.cuda.nvtx.range(name) if self.nvtx else contextlib.nullcontext()
 
+    def _selects(self):
+        if self.dense:
+            raise ValueError("a dense step has no indexer and no top-k")
+
     def indexer(self, stream=None):
+        self._selects()
         with self._range("dsa_indexer_logits"):
             self._indexer(stream)
 
     def topk(self, stream=None):
+        self._selects()
         with self._range("dsa_topk"):
             self._topk(stream)
 
@@ -166,8 +176,8 @@ class DsaStep:
         return self.out
 
     def run_host(self, host_inputs, host_q, host_outputs):
-        """One step from pinned host memory on the current stream: the
-        indexer's inputs (`host_inputs`, laid out like `inputs`) are copied
+        """One step from pinned host memory on the current stream: the step's
+        inputs but q (`host_inputs`, laid out like `inputs`) are copied
         first; the attention queries (`host_q`, like `inputs_q`) are copied on
         a side stream while the indexer and top-k run; out and lse come back
         into `host_outputs` (like `outputs`)."""
