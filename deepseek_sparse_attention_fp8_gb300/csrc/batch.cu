@@ -219,7 +219,13 @@ extern "C" dsa_status_t dsa_build_batch(const int32_t* ctx_lens, const int32_t* 
     return fail(DSA_ERR_INVALID_ARG, "dsa_build_batch: free_blocks without free_head and free_head_out");
   if (!free_blocks && num_free > 0)
     return fail(DSA_ERR_INVALID_ARG, "dsa_build_batch: num_free without free_blocks");
-  if (B > 0 && (seq_lens == ctx_lens || seq_lens == new_lens || query_start_loc == ctx_lens || query_start_loc == new_lens))
+  // (every CTA reads all lengths, at any time)
+  const auto share = [B](const int32_t* out, int64_t n, const int32_t* in) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(in);
+    return a < b + 4 * static_cast<uintptr_t>(B) && b < a + 4 * static_cast<uintptr_t>(n);
+  };
+  if (share(seq_lens, B, ctx_lens) || share(seq_lens, B, new_lens) ||
+      share(query_start_loc, int64_t(B) + 1, ctx_lens) || share(query_start_loc, int64_t(B) + 1, new_lens))
     return fail(DSA_ERR_INVALID_ARG, "dsa_build_batch: seq_lens and query_start_loc must not share the inputs' memory");
   dsa_status_t st = check_device();
   if (st != DSA_OK) return st;
