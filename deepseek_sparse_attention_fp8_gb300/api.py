@@ -442,7 +442,8 @@ def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, fre
     (seq_lens [B], query_start_loc [B+1], token_req, positions, slot_map
     [max_tokens]) and grows block_table [B, bt_stride] in place by blocks of
     the queue free_blocks, from *free_head on; free_head_out (default: in
-    place) receives the advanced head."""
+    place) receives the advanced head. Result buffers that are given may be
+    longer: what lies behind their part is left as it was, and not returned."""
     i32, dev = torch.int32, torch.cuda.current_device()
     ctx_p, new_p = _vec(ctx_lens, i32, 0, "ctx_lens", dev), _vec(new_lens, i32, 0, "new_lens", dev)
     table_p = _arg(block_table, i32, 2, "block_table", dev)
@@ -474,7 +475,8 @@ def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, fre
                              head_p, head_out_p, table_p, table_cols, max_tokens, seq_p, qsl_p, req_p, pos_p,
                              slot_p, _status_arg(dev_status, dev), _raw_stream(stream, dev))
     _check(st, "dsa_build_batch")
-    return seq_lens, query_start_loc, token_req, positions, slot_map
+    return tuple(t if t.shape[0] == m else t[:m] for t, m in ((seq_lens, B), (query_start_loc, B + 1), (token_req, n),
+                                                              (positions, n), (slot_map, n)))
 
 
 def dsa_mla_kv_cache(kv, slot_map, kv_cache, dev_status=None, stream=None):
