@@ -475,8 +475,17 @@ def dsa_build_batch(ctx_lens, new_lens, block_table, block_size, max_tokens, fre
                              head_p, head_out_p, table_p, table_cols, max_tokens, seq_p, qsl_p, req_p, pos_p,
                              slot_p, _status_arg(dev_status, dev), _raw_stream(stream, dev))
     _check(st, "dsa_build_batch")
-    return tuple(t if t.shape[0] == m else t[:m] for t, m in ((seq_lens, B), (query_start_loc, B + 1), (token_req, n),
-                                                              (positions, n), (slot_map, n)))
+    if seq_lens.numel() != B:
+        seq_lens = seq_lens[:B]
+    if query_start_loc.numel() != B + 1:
+        query_start_loc = query_start_loc[:B + 1]
+    if token_req.numel() != n:
+        token_req = token_req[:n]
+    if positions.numel() != n:
+        positions = positions[:n]
+    if slot_map.numel() != n:
+        slot_map = slot_map[:n]
+    return seq_lens, query_start_loc, token_req, positions, slot_map
 
 
 def dsa_mla_kv_cache(kv, slot_map, kv_cache, dev_status=None, stream=None):

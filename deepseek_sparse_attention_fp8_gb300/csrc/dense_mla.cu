@@ -14,8 +14,9 @@
 //   clusters of 4  (dense_mla_quad.cu)  256 rows: chunks over long contexts;
 //                  they work as two pairs each where that is faster.
 // A row tile cut by a run's end leaves fp32 partials, at most two per run, which
-// dense_mla_merge_kernel joins. It reads 31 MB in ~5 us behind 32 requests of
-// 8192 keys and 128 heads, where every run of 27 steps is cut.
+// dense_mla_merge_kernel joins. Behind 32 requests of 8192 keys and 128 heads, in
+// runs of 27 steps, it reads 28 MB of them (106 parts) and takes, with its launch,
+// 10 of the call's 95 us (caches cold).
 #include <algorithm>
 
 #include "dense_mla_pair.cuh"

@@ -301,7 +301,7 @@ struct Decoder {
 // costs a pair about 7100 + 4400 clocks a step (128 rows, 2 SMs), a quad 12300
 // + 2700 (256 rows, 4 SMs) and ~12000 more to begin with: fitted to 16 prompts
 // of 256 tokens (128 heads: 380 us on pairs, 477 on quads) and to 1024 tokens
-// over a context of 16384 (3580 and 2600 us). Between: 64 x 2 tokens over 4096
+// over a context of 16384 (3580 and 2600 us, single launches). Between: 64 x 2 tokens over 4096
 // keys 156 and 125, 8 x 16 over 2048 84 and 83, 32 x 2 over 2048 56 and 61.
 // Pairs in clusters of four (144 of 152 SMs, and this choice) take 5-9% longer
 // than launched as pairs.

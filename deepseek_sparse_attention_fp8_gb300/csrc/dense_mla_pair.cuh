@@ -18,13 +18,13 @@
 // (measured: 131 clocks at N = 256, 82 at N = 128), 36 and 16 of them a step; a
 // step also moves 104 KB into each SM, 3330 clocks at the ~32 bytes a clock that
 // an SM takes in (measured: 62 GB/s, from L2 or memory, multicast or not). A
-// step takes 4400-4800 clocks. 32 requests of 8192 keys, 128 heads: 85 us; 8 of
-// 131072: 277 us (floors: 46 and 178 by bytes). Of the 85, about 10 pass until
+// step takes 4400-4800 clocks. 32 requests of 8192 keys, 128 heads: 86 us; 8 of
+// 131072: 279 us (floors: 46 and 178 by bytes). Of the 86, about 10 pass until
 // the first S (the plan, the table, 208 KB from memory into every pair), 6 go
-// into partials and 5 into joining them.
+// into partials and 10 into joining them, a launch included.
 // With the fp8 cache codes are copied to where half of their values belong and
 // decoded in place: one more stage between a slot's being free and its MMA, and
-// only two steps are in flight. 32 requests of 8192 keys: 103 us, 98 without the
+// only two steps are in flight. 32 requests of 8192 keys: 104 us, 98 without the
 // arithmetic of decoding, 2 more without asking rows into L2 ahead.
 //
 // Work: the steps of all row tiles form one sequence, cut into equal runs, one

@@ -16,14 +16,16 @@
 // KB of P (CTAs 2, 3): ~3000 clocks at the ~32 bytes per clock that an SM
 // takes in, against 2300 and 2050 of MMA, for twice the rows of a pair's step.
 // Measured: 2600-2800 clocks a step; 1024 tokens over a context of 16384 (128
-// heads) 2.67 ms, 1.69 PFLOP/s or 0.91 of the measured tensor rate, with 9.0
-// TB/s taken in by the 144 SMs in use: both are nearly full (pairs: 3.58 ms).
+// heads) 2.69 ms, 1.68 PFLOP/s or 0.90 of the measured tensor rate; a launch by
+// itself 2.49 ms, with 8.9 TB/s taken in by the 144 SMs in use: both are nearly
+// full (pairs: 3.58 ms).
 // With the fp8 cache CTAs 0, 1 decode their 64 keys, CTAs 2, 3 their dims of
 // all keys. Codes are copied to where half of their values belong and decoded
-// in place. Five chunks of up to 700 tokens over up to 9000 keys: 1.70 ms (1.45
-// without the arithmetic of decoding). With the codes loaded into registers a
-// step ahead it was 1.80, and 1.43 without those loads: the few KB of L1 beside
-// 227 KB of shared memory hold too few lines in flight.
+// in place. Five chunks of up to 700 tokens over up to 9000 keys: 1.75 ms (1.70
+// before the odd CTAs' slots were handed on in order, then 1.45 without the
+// arithmetic of decoding). With the codes loaded into registers a step ahead it
+// was 1.80, and 1.43 without those loads: the few KB of L1 beside 227 KB of
+// shared memory hold too few lines in flight.
 #include <algorithm>
 
 #include "dense_mla_pair.cuh"

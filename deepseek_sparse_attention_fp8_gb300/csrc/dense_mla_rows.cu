@@ -18,7 +18,8 @@
 // and decoded in place, a slot of 128 keys x 128 dims at a time. 64 requests of
 // 4096 keys, 16 heads (172 MB, 25 us): 87 us, 110 on pairs; 82 without the
 // arithmetic of decoding. Decoding from loads into registers a step ahead took
-// 108, 77 without those loads.
+// 108, 77 without those loads. 14 warps leave a thread 128 registers, and one is
+// spilled (4 bytes stored, 16 loaded).
 //
 // Rope dims come first in a step: their slots are free again after S, so that a
 // third of the next step is loaded while this one's weights are made. Results
