@@ -64,8 +64,9 @@ DSA_STEPS_FN int64_t floor_sum(int64_t n, int64_t a, int64_t b) {
     const int64_t b0 = b / a;
     return upto(n + b0) - upto(b0);
   }
-  // the lattice points under the line: whole multiples are taken out of a and b,
-  // then the axes change places, as in Euclid's algorithm for (a, 128)
+  // the well-known count of the lattice points under a line by the steps of
+  // Euclid's algorithm, here for (a, 128): whole multiples are taken out of a and
+  // b, then the axes change places
   int64_t sum = 0, m = 128;
   while (true) {
     sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
